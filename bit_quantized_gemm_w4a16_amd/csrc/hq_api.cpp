@@ -8,6 +8,7 @@
 // spirit of the launch-overhead work in "Humming v0.1.0-0.1.4", section
 // "v0.1.1".
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -16,6 +17,7 @@
 
 #include "hq_common.h"
 #include "hq_internal.h"
+#include "hq_kv.h"
 
 namespace hq {
 
@@ -413,6 +415,90 @@ static hq_status scratch_for_stream(hipStream_t stream, void** out) {
     return HQ_OK;
 }
 
+// ---------------------------------------------------------------------------
+// paged key/value cache: descriptor checks
+// ---------------------------------------------------------------------------
+
+static bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+static hq_status describe_kv(const hq_kv_desc* d, KvLayout* L) {
+    if (!d) return set_error(HQ_ERR_INVALID_ARG, "kv descriptor is NULL");
+    if (d->abi_version != HQ_ABI_VERSION) return set_error(HQ_ERR_ABI, "kv abi_version %d, library has %d", d->abi_version, HQ_ABI_VERSION);
+    if (d->reserved) return set_error(HQ_ERR_INVALID_ARG, "kv reserved field must be zero");
+    if (d->dtype != HQ_DT_BF16 && d->dtype != HQ_DT_FP16 && d->dtype != HQ_DT_FP8_E4M3)
+        return set_error(HQ_ERR_UNSUPPORTED, "cache dtype %d (BF16, FP16 or FP8_E4M3)", d->dtype);
+    if (d->block_size < 1 || d->block_size > 65536 || d->num_blocks < 1 || d->num_blocks > 0x7FFFFFFFLL)
+        return set_error(HQ_ERR_INVALID_ARG, "block_size %d or num_blocks %lld out of range", d->block_size, (long long)d->num_blocks);
+    if (d->num_blocks * d->block_size > 0x7FFFFFFFLL)
+        return set_error(HQ_ERR_UNSUPPORTED, "num_blocks * block_size must stay below 2^31");
+    if (d->kv_heads < 1 || d->kv_heads > 1024) return set_error(HQ_ERR_INVALID_ARG, "kv_heads %d out of range", d->kv_heads);
+    if (d->head_dim < 16 || d->head_dim > 256 || d->head_dim % 16)
+        return set_error(HQ_ERR_UNSUPPORTED, "head_dim %d (a multiple of 16, 16..256)", d->head_dim);
+    const int64_t st[3] = {d->block_stride, d->slot_stride, d->head_stride};
+    for (int64_t s : st)
+        if (s < 16 || s % 16 || s > ((int64_t)1 << 40))
+            return set_error(HQ_ERR_INVALID_ARG, "cache stride %lld (a positive multiple of 16)", (long long)s);
+    if ((d->block_stride >> 8) * d->num_blocks > ((int64_t)1 << 40))
+        return set_error(HQ_ERR_UNSUPPORTED, "the cache spans more than 2^48 elements");
+    *L = KvLayout{d->block_stride, d->slot_stride, d->head_stride, d->num_blocks, d->kv_heads, d->head_dim, d->block_size,
+                  FastDiv::of((uint32_t)d->block_size), d->dtype};
+    return HQ_OK;
+}
+
+static hq_status check_rope(const hq_rope_desc* d) {
+    if (!d) return set_error(HQ_ERR_INVALID_ARG, "rope descriptor is NULL");
+    if (d->abi_version != HQ_ABI_VERSION) return set_error(HQ_ERR_ABI, "rope abi_version %d, library has %d", d->abi_version, HQ_ABI_VERSION);
+    if (d->rot_dim < 16 || d->rot_dim > 256 || d->rot_dim % 16)
+        return set_error(HQ_ERR_UNSUPPORTED, "rot_dim %d (a multiple of 16, 16..256)", d->rot_dim);
+    if (d->layout != HQ_ROPE_HALF && d->layout != HQ_ROPE_INTERLEAVED) return set_error(HQ_ERR_INVALID_ARG, "bad rope layout %d", d->layout);
+    if (d->scaling < HQ_ROPE_NONE || d->scaling > HQ_ROPE_PARTS) return set_error(HQ_ERR_INVALID_ARG, "bad rope scaling %d", d->scaling);
+    if (!(d->base > 1.0) || !std::isfinite(d->base)) return set_error(HQ_ERR_INVALID_ARG, "rope base must be above 1");
+    if (d->scaling != HQ_ROPE_NONE && (!(d->factor >= 1.0) || !std::isfinite(d->factor)))
+        return set_error(HQ_ERR_INVALID_ARG, "rope factor must be at least 1");
+    if (d->scaling == HQ_ROPE_PARTS) {
+        if (!(d->context >= 1.0) || !std::isfinite(d->context)) return set_error(HQ_ERR_INVALID_ARG, "rope context must be at least 1");
+        if (!(d->fast > d->slow) || !std::isfinite(d->fast) || !std::isfinite(d->slow))
+            return set_error(HQ_ERR_INVALID_ARG, "rope fast must be above slow");
+        if (!(d->attn_factor >= 0.0) || !std::isfinite(d->attn_factor)) return set_error(HQ_ERR_INVALID_ARG, "rope attn_factor out of range");
+    } else if (d->attn_factor != 0.0) {
+        return set_error(HQ_ERR_INVALID_ARG, "attn_factor belongs to HQ_ROPE_PARTS");
+    }
+    return HQ_OK;
+}
+
+// Sizes of an attention call into `a` (no pointers).
+static hq_status describe_attn(const hq_attn_desc* d, const hq_kv_desc* kv, int64_t B, int64_t T, int64_t prefix_len, AttnArgs* a) {
+    *a = AttnArgs{};
+    if (!d) return set_error(HQ_ERR_INVALID_ARG, "attention descriptor is NULL");
+    if (d->abi_version != HQ_ABI_VERSION) return set_error(HQ_ERR_ABI, "attention abi_version %d, library has %d", d->abi_version, HQ_ABI_VERSION);
+    if (d->reserved) return set_error(HQ_ERR_INVALID_ARG, "attention reserved field must be zero");
+    const hq_status st = describe_kv(kv, &a->kv);
+    if (st != HQ_OK) return st;
+    if (d->dtype != HQ_DT_BF16 && d->dtype != HQ_DT_FP16) return set_error(HQ_ERR_UNSUPPORTED, "attention dtype %d (BF16 or FP16)", d->dtype);
+    if (kv->dtype != HQ_DT_FP8_E4M3 && kv->dtype != d->dtype)
+        return set_error(HQ_ERR_UNSUPPORTED, "a 16-bit cache must have the dtype of q");
+    if (d->q_heads < 1 || d->q_heads > 4096 || d->q_heads % kv->kv_heads)
+        return set_error(HQ_ERR_INVALID_ARG, "q_heads %d must be a multiple of kv_heads %d (up to 4096)", d->q_heads, kv->kv_heads);
+    if (B < 0 || B > (1 << 20) || T < 0 || T > (1 << 23)) return set_error(HQ_ERR_INVALID_ARG, "B or T out of range");
+    if (d->max_new < 1 || d->max_new > (1 << 23) || d->max_kv < 0 || d->max_kv > (1 << 29) || prefix_len < 0 || prefix_len > (1 << 29))
+        return set_error(HQ_ERR_INVALID_ARG, "max_new, max_kv or prefix_len out of range");
+    if (d->total_kv < 0) return set_error(HQ_ERR_INVALID_ARG, "total_kv is negative");
+    if (T * d->q_heads >= ((int64_t)1 << 30)) return set_error(HQ_ERR_UNSUPPORTED, "T * q_heads must stay below 2^30");
+    if (!(d->scale > 0.f) || !std::isfinite(d->scale)) return set_error(HQ_ERR_INVALID_ARG, "scale must be positive");
+    if (!(d->softcap >= 0.f) || !std::isfinite(d->softcap)) return set_error(HQ_ERR_INVALID_ARG, "softcap must be 0 or positive");
+    a->bf16 = d->dtype == HQ_DT_BF16;
+    a->q_heads = d->q_heads;
+    a->B = B;
+    a->T = T;
+    a->prefix_len = prefix_len;
+    a->max_new = d->max_new < T ? d->max_new : T;
+    a->max_kv = d->max_kv;
+    a->total_kv = d->total_kv < B * d->max_kv ? d->total_kv : B * d->max_kv;
+    a->scale = d->scale;
+    a->softcap = d->softcap;
+    return HQ_OK;
+}
+
 }  // namespace hq
 
 using namespace hq;
@@ -707,6 +793,195 @@ hq_status hq_silu_mul(int32_t dtype, int64_t rows, int64_t I, const void* gate_u
     if (!gate_up || !out) return set_error(HQ_ERR_INVALID_ARG, "gate_up and out are required");
     if (!aligned16(gate_up) || !aligned16(out)) return set_error(HQ_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
     return hip_status(silu_mul_launch(rows, I, gate_up, out, (hipStream_t)stream), "hq_silu_mul");
+}
+
+hq_status hq_kv_slots(int32_t block_size, int64_t B, int64_t T_cap, int64_t max_blocks, int64_t first_pos,
+                      const int32_t* cached_lens, const int32_t* new_lens, const int32_t* free_blocks, int64_t n_free,
+                      int32_t* block_table, int32_t* cu_new, int32_t* kv_lens, int32_t* positions, int64_t* slots,
+                      int32_t* taken, hq_stream_t stream) {
+    if (block_size < 1 || block_size > 65536) return set_error(HQ_ERR_INVALID_ARG, "block_size %d out of range", block_size);
+    if (B < 0 || T_cap < 0 || T_cap > (1LL << 30) || max_blocks < 0 || max_blocks > (1LL << 30) || n_free < 0 || n_free > (1LL << 31) - 1 ||
+        first_pos < 0 || first_pos > (1LL << 30))
+        return set_error(HQ_ERR_INVALID_ARG, "B, T_cap, max_blocks, n_free or first_pos out of range");
+    if (B > HQ_KV_MAX_REQUESTS) return set_error(HQ_ERR_UNSUPPORTED, "B=%lld exceeds %d requests", (long long)B, HQ_KV_MAX_REQUESTS);
+    if (!cu_new || !taken || (B && (!cached_lens || !new_lens || !kv_lens)) || (B && max_blocks && !block_table) || (n_free && !free_blocks) ||
+        (T_cap && (!positions || !slots)))
+        return set_error(HQ_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned(cached_lens, 4) || !aligned(new_lens, 4) || !aligned(free_blocks, 4) || !aligned(block_table, 4) || !aligned(cu_new, 4) ||
+        !aligned(kv_lens, 4) || !aligned(positions, 4) || !aligned(slots, 8) || !aligned(taken, 4))
+        return set_error(HQ_ERR_ALIGNMENT, "an integer buffer is not aligned to its elements");
+    KvSlotsArgs a{block_size, FastDiv::of((uint32_t)block_size), B, T_cap, max_blocks, first_pos, n_free, cached_lens, new_lens, free_blocks,
+                  block_table, cu_new, kv_lens, positions, taken, slots, (hipStream_t)stream};
+    return hip_status(kv_slots_launch(a), "hq_kv_slots");
+}
+
+hq_status hq_rope_table(const hq_rope_desc* rope, int64_t first_pos, int64_t count, float* table, hq_stream_t stream) {
+    const hq_status st = check_rope(rope);
+    if (st != HQ_OK) return st;
+    if (first_pos < 0 || count < 0 || first_pos > (1LL << 31) || count > (1LL << 31) || first_pos + count > (1LL << 31))
+        return set_error(HQ_ERR_INVALID_ARG, "first_pos or count out of range");
+    if (count == 0) return ok();
+    if (!table) return set_error(HQ_ERR_INVALID_ARG, "table is required");
+    if (!aligned16(table)) return set_error(HQ_ERR_ALIGNMENT, "table must be 16-byte aligned");
+    RopeTableArgs a;
+    const double rot = rope->rot_dim, pi2 = 6.283185307179586476925286766559;
+    const double base = rope->scaling == HQ_ROPE_NTK ? rope->base * std::pow(rope->factor, rot / (rot - 2.0)) : rope->base;
+    a.gain = 1.0;
+    if (rope->scaling == HQ_ROPE_PARTS) a.gain = rope->attn_factor > 0.0 ? rope->attn_factor : 0.1 * std::log(rope->factor) + 1.0;
+    a.half = rope->rot_dim / 2;
+    for (int d = 0; d < a.half; ++d) {
+        double f = std::pow(base, -2.0 * d / rot);
+        if (rope->scaling == HQ_ROPE_LINEAR) f /= rope->factor;
+        if (rope->scaling == HQ_ROPE_PARTS) {
+            double g = (rope->context * f / pi2 - rope->slow) / (rope->fast - rope->slow);
+            g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+            f = f * g + f / rope->factor * (1.0 - g);
+        }
+        a.turns[d] = f / pi2;
+    }
+    a.first = first_pos;
+    a.count = count;
+    a.table = table;
+    a.stream = (hipStream_t)stream;
+    return hip_status(rope_table_launch(a), "hq_rope_table");
+}
+
+hq_status hq_rope_kv(const hq_rope_desc* rope, const hq_kv_desc* kv, int32_t dtype, int64_t T, int32_t q_heads,
+                     const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                     const int32_t* positions, const float* table, int64_t table_rows, const int64_t* slots,
+                     void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache, const float* k_scale,
+                     const float* v_scale, hq_stream_t stream) {
+    hq_status st = check_rope(rope);
+    if (st != HQ_OK) return st;
+    RopeKvArgs a{};
+    st = describe_kv(kv, &a.kv);
+    if (st != HQ_OK) return st;
+    if (dtype != HQ_DT_BF16 && dtype != HQ_DT_FP16) return set_error(HQ_ERR_UNSUPPORTED, "dtype %d (BF16 or FP16)", dtype);
+    const bool fp8 = kv->dtype == HQ_DT_FP8_E4M3;
+    if (!fp8 && kv->dtype != dtype) return set_error(HQ_ERR_UNSUPPORTED, "a 16-bit cache must have the dtype of q");
+    if (rope->rot_dim > kv->head_dim) return set_error(HQ_ERR_INVALID_ARG, "rot_dim %d exceeds head_dim %d", rope->rot_dim, kv->head_dim);
+    if (q_heads < 1 || q_heads > 4096) return set_error(HQ_ERR_INVALID_ARG, "q_heads %d out of range", q_heads);
+    if (T < 0 || T > (1 << 23) || table_rows < 1 || table_rows > (1LL << 31)) return set_error(HQ_ERR_INVALID_ARG, "T or table_rows out of range");
+    const int64_t qr = (int64_t)q_heads * kv->head_dim, kr = (int64_t)kv->kv_heads * kv->head_dim;
+    if (q_stride < qr || q_out_stride < qr || k_stride < kr || v_stride < kr || q_stride % 8 || q_out_stride % 8 || k_stride % 8 || v_stride % 8)
+        return set_error(HQ_ERR_INVALID_ARG, "row strides must be multiples of 8 and hold a row");
+    if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr))
+        return set_error(HQ_ERR_INVALID_ARG, fp8 ? "k_scale and v_scale required for an E4M3 cache" : "scales must be NULL for a 16-bit cache");
+    if (T == 0) return ok();
+    if (!q || !k || !v || !positions || !table || !slots || !q_out || !k_cache || !v_cache)
+        return set_error(HQ_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(table) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache))
+        return set_error(HQ_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+    if (!aligned(positions, 4) || !aligned(slots, 8) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return set_error(HQ_ERR_ALIGNMENT, "positions, slots or a scale is not aligned to its elements");
+    if (q == q_out && q_stride != q_out_stride) return set_error(HQ_ERR_INVALID_ARG, "q in place needs one stride");
+    a.bf16 = dtype == HQ_DT_BF16;
+    a.interleaved = rope->layout == HQ_ROPE_INTERLEAVED;
+    a.rot = rope->rot_dim;
+    a.q_heads = q_heads;
+    a.T = T;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out_stride = q_out_stride;
+    a.table_rows = table_rows;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.positions = positions;
+    a.table = table;
+    a.slots = slots;
+    a.q_out = q_out;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.stream = (hipStream_t)stream;
+    return hip_status(rope_kv_launch(a), "hq_rope_kv");
+}
+
+static hq_status attn_need(const AttnArgs& a, size_t* bytes) {
+    *bytes = a.T && a.B ? attn_workspace(a) : 0;
+    if (*bytes == SIZE_MAX) return set_error(HQ_ERR_UNSUPPORTED, "more workgroups than one launch holds");
+    return HQ_OK;
+}
+
+hq_status hq_attn_workspace_bytes(const hq_attn_desc* desc, const hq_kv_desc* kv, int64_t B, int64_t T,
+                                  int64_t prefix_len, size_t* bytes) {
+    AttnArgs a;
+    hq_status st = describe_attn(desc, kv, B, T, prefix_len, &a);
+    if (st != HQ_OK) return st;
+    if (!bytes) return set_error(HQ_ERR_INVALID_ARG, "bytes is NULL");
+    st = attn_need(a, bytes);
+    return st == HQ_OK ? ok() : st;
+}
+
+hq_status hq_attn_plan(const hq_attn_desc* desc, const hq_kv_desc* kv, int64_t B, int64_t T, int64_t prefix_len, char* buf,
+                       size_t len) {
+    AttnArgs a;
+    hq_status st = describe_attn(desc, kv, B, T, prefix_len, &a);
+    if (st != HQ_OK) return st;
+    if (!buf || len < 2) return set_error(HQ_ERR_INVALID_ARG, "buf must hold at least 2 bytes");
+    buf[0] = 0;
+    size_t need;
+    st = attn_need(a, &need);
+    if (st != HQ_OK) return st;
+    if (T == 0 || B == 0) return ok();
+    PlanRecorder rec{buf, len, 0, 0, 0};
+    g_plan = &rec;
+    const hipError_t e = attn_launch(a);
+    g_plan = nullptr;
+    return hip_status(e, "hq_attn_plan");
+}
+
+hq_status hq_attn(const hq_attn_desc* desc, const hq_kv_desc* kv, int64_t B, int64_t T, const void* q, int64_t q_stride,
+                  const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                  const int32_t* prefix_table, int64_t prefix_len, const int32_t* block_table, int64_t max_blocks,
+                  const int32_t* kv_lens, const int32_t* cu_new, void* out, int64_t out_stride, float* lse,
+                  void* workspace, size_t ws_bytes, hq_stream_t stream) {
+    AttnArgs a;
+    hq_status st = describe_attn(desc, kv, B, T, prefix_len, &a);
+    if (st != HQ_OK) return st;
+    const int64_t row = (int64_t)desc->q_heads * kv->head_dim;
+    if (q_stride < row || out_stride < row || q_stride % 8 || out_stride % 8)
+        return set_error(HQ_ERR_INVALID_ARG, "row strides must be multiples of 8 and hold a row");
+    const bool fp8 = kv->dtype == HQ_DT_FP8_E4M3;
+    if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr))
+        return set_error(HQ_ERR_INVALID_ARG, fp8 ? "k_scale and v_scale required for an E4M3 cache" : "scales must be NULL for a 16-bit cache");
+    if (max_blocks < 0 || max_blocks > (1LL << 30)) return set_error(HQ_ERR_INVALID_ARG, "max_blocks out of range");
+    if (T == 0 || B == 0) return ok();
+    if (!q || !k_cache || !v_cache || !kv_lens || !cu_new || !out || (prefix_len && !prefix_table) || (max_blocks && !block_table))
+        return set_error(HQ_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+        return set_error(HQ_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+    if (!aligned(prefix_table, 4) || !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(cu_new, 4) || !aligned(lse, 4) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return set_error(HQ_ERR_ALIGNMENT, "a table, length, scale or lse buffer is not aligned to its elements");
+    size_t need;
+    st = attn_need(a, &need);
+    if (st != HQ_OK) return st;
+    if (need) {
+        if (!workspace || ws_bytes < need)
+            return set_error(HQ_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given", need, workspace ? ws_bytes : (size_t)0);
+        if (!aligned16(workspace)) return set_error(HQ_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+    }
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.max_blocks = max_blocks;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.prefix_table = prefix_table;
+    a.block_table = block_table;
+    a.kv_lens = kv_lens;
+    a.cu = cu_new;
+    a.out = out;
+    a.lse = lse;
+    a.ws = workspace;
+    a.stream = (hipStream_t)stream;
+    return hip_status(attn_launch(a), "hq_attn");
 }
 
 hq_status hq_probe_stream(const void* src, size_t bytes, void* sink, int32_t reps, hq_stream_t stream) {

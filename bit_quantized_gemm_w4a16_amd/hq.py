@@ -31,6 +31,9 @@ HQ_ASCALE_NONE, HQ_ASCALE_PER_TOKEN_F32, HQ_ASCALE_MX_E8M0, HQ_ASCALE_PER_BLOCK1
 HQ_S2_NONE, HQ_S2_PER_TENSOR_F32 = 0, 1
 HQ_MOE_INDEXED, HQ_MOE_GROUPED = 1, 2
 HQ_FLAG_BATCH_INVARIANT = 1
+HQ_ROPE_HALF, HQ_ROPE_INTERLEAVED = 1, 2
+HQ_ROPE_NONE, HQ_ROPE_LINEAR, HQ_ROPE_NTK, HQ_ROPE_PARTS = range(4)
+HQ_KV_MAX_REQUESTS = 4096
 HQ_TUNE_STREAM, HQ_TUNE_T128, HQ_TUNE_T256, HQ_TUNE_W128, HQ_TUNE_W256, HQ_TUNE_STREAM8 = 1, 2, 3, 4, 5, 6
 
 
@@ -52,6 +55,29 @@ class hq_layer_desc(C.Structure):
         ("w_scale_dtype", C.c_int32), ("w_scale_gran", C.c_int32), ("group_size", C.c_int32),
         ("zp_dtype", C.c_int32), ("scale2", C.c_int32), ("out_dtype", C.c_int32),
         ("flags", C.c_int32), ("tune", C.c_int32), ("reserved", C.c_int32),
+    ]
+
+
+class hq_kv_desc(C.Structure):
+    _fields_ = [
+        ("abi_version", C.c_int32), ("dtype", C.c_int32), ("num_blocks", C.c_int64), ("block_size", C.c_int32),
+        ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("reserved", C.c_int32),
+        ("block_stride", C.c_int64), ("slot_stride", C.c_int64), ("head_stride", C.c_int64),
+    ]
+
+
+class hq_rope_desc(C.Structure):
+    _fields_ = [
+        ("abi_version", C.c_int32), ("rot_dim", C.c_int32), ("layout", C.c_int32), ("scaling", C.c_int32),
+        ("base", C.c_double), ("factor", C.c_double), ("context", C.c_double), ("slow", C.c_double), ("fast", C.c_double),
+        ("attn_factor", C.c_double),
+    ]
+
+
+class hq_attn_desc(C.Structure):
+    _fields_ = [
+        ("abi_version", C.c_int32), ("dtype", C.c_int32), ("q_heads", C.c_int32), ("reserved", C.c_int32),
+        ("max_new", C.c_int64), ("max_kv", C.c_int64), ("total_kv", C.c_int64), ("scale", C.c_float), ("softcap", C.c_float),
     ]
 
 
@@ -78,6 +104,15 @@ _SIGS = {
     "hq_moe_align": (C.c_int, [C.c_int64, C.c_int32, C.c_int32, _P, _P, _P, _P, C.c_size_t, _P]),
     "hq_moe_gather": (C.c_int, [C.c_int32, C.c_int64, C.c_int32, C.c_int64, _P, _P, _P, _P]),
     "hq_silu_mul": (C.c_int, [C.c_int32, C.c_int64, C.c_int64, _P, _P, _P]),
+    "hq_kv_slots": (C.c_int, [C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_int64, _P, _P, _P, C.c_int64, _P, _P, _P, _P,
+                              _P, _P, _P]),
+    "hq_rope_table": (C.c_int, [_P, C.c_int64, C.c_int64, _P, _P]),
+    "hq_rope_kv": (C.c_int, [_P, _P, C.c_int32, C.c_int64, C.c_int32, _P, C.c_int64, _P, C.c_int64, _P, C.c_int64, _P, _P,
+                             C.c_int64, _P, _P, C.c_int64, _P, _P, _P, _P, _P]),
+    "hq_attn_workspace_bytes": (C.c_int, [_P, _P, C.c_int64, C.c_int64, C.c_int64, _P]),
+    "hq_attn_plan": (C.c_int, [_P, _P, C.c_int64, C.c_int64, C.c_int64, C.c_char_p, C.c_size_t]),
+    "hq_attn": (C.c_int, [_P, _P, C.c_int64, C.c_int64, _P, C.c_int64, _P, _P, _P, _P, _P, C.c_int64, _P, C.c_int64, _P,
+                          _P, _P, C.c_int64, _P, _P, C.c_size_t, _P]),
     "hq_probe_stream": (C.c_int, [_P, C.c_size_t, _P, C.c_int32, _P]),
     "hq_probe_mfma": (C.c_int, [C.c_int32, C.c_int64, C.c_int32, _P, _P]),
 }
@@ -239,6 +274,33 @@ def desc_moe_mxfp4(E, N, K) -> hq_layer_desc:
                      num_experts=E)
 
 
+def kv_desc(dtype, num_blocks, block_size, kv_heads, head_dim, head_major=False) -> hq_kv_desc:
+    """A dense paged cache: pages of [token][head][element], or [head][token][element] (head_major)."""
+    d = hq_kv_desc()
+    d.abi_version, d.dtype = HQ_ABI_VERSION, dtype
+    d.num_blocks, d.block_size, d.kv_heads, d.head_dim = num_blocks, block_size, kv_heads, head_dim
+    d.block_stride = block_size * kv_heads * head_dim
+    d.slot_stride = head_dim if head_major else kv_heads * head_dim
+    d.head_stride = block_size * head_dim if head_major else head_dim
+    return d
+
+
+def rope_desc(rot_dim, base=10000.0, interleaved=False, scaling=HQ_ROPE_NONE, factor=1.0, context=0, slow=1.0, fast=32.0,
+              attn_factor=0.0) -> hq_rope_desc:
+    d = hq_rope_desc()
+    d.abi_version, d.rot_dim = HQ_ABI_VERSION, rot_dim
+    d.layout, d.scaling = HQ_ROPE_INTERLEAVED if interleaved else HQ_ROPE_HALF, scaling
+    d.base, d.factor, d.context, d.slow, d.fast, d.attn_factor = base, factor, context, slow, fast, attn_factor
+    return d
+
+
+def attn_desc(dtype, q_heads, max_new, max_kv, scale, softcap=0.0, total_kv=0) -> hq_attn_desc:
+    d = hq_attn_desc()
+    d.abi_version, d.dtype, d.q_heads = HQ_ABI_VERSION, dtype, q_heads
+    d.max_new, d.max_kv, d.total_kv, d.scale, d.softcap = max_new, max_kv, total_kv, scale, softcap
+    return d
+
+
 # ---------------------------------------------------------------------------
 # entry points (same names as the C ABI)
 # ---------------------------------------------------------------------------
@@ -351,3 +413,42 @@ def hq_probe_mfma(dtype, workgroups, iters, sink, stream=None) -> float:
 
 def hq_silu_mul(dtype, rows, I, gate_up, out, stream=None) -> None:
     _check(lib().hq_silu_mul(dtype, rows, I, _dp(gate_up), _dp(out), _stream(stream)), "hq_silu_mul")
+
+
+def hq_kv_slots(block_size, B, T_cap, cached_lens, new_lens, free_blocks, n_free, block_table, max_blocks, cu_new, kv_lens,
+                positions, slots, taken, first_pos=0, stream=None) -> None:
+    _check(lib().hq_kv_slots(block_size, B, T_cap, max_blocks, first_pos, _dp(cached_lens), _dp(new_lens), _dp(free_blocks),
+                             n_free, _dp(block_table), _dp(cu_new), _dp(kv_lens), _dp(positions), _dp(slots), _dp(taken),
+                             _stream(stream)), "hq_kv_slots")
+
+
+def hq_rope_table(rope, first_pos, count, table, stream=None) -> None:
+    _check(lib().hq_rope_table(C.byref(rope), first_pos, count, _dp(table), _stream(stream)), "hq_rope_table")
+
+
+def hq_rope_kv(rope, kv, dtype, T, q_heads, q, q_stride, k, k_stride, v, v_stride, positions, table, table_rows, slots, q_out,
+               q_out_stride, k_cache, v_cache, k_scale=None, v_scale=None, stream=None) -> None:
+    _check(lib().hq_rope_kv(C.byref(rope), C.byref(kv), dtype, T, q_heads, _dp(q), q_stride, _dp(k), k_stride, _dp(v),
+                            v_stride, _dp(positions), _dp(table), table_rows, _dp(slots), _dp(q_out), q_out_stride,
+                            _dp(k_cache), _dp(v_cache), _dp(k_scale), _dp(v_scale), _stream(stream)), "hq_rope_kv")
+
+
+def hq_attn_workspace_bytes(desc, kv, B, T, prefix_len) -> int:
+    b = C.c_size_t()
+    _check(lib().hq_attn_workspace_bytes(C.byref(desc), C.byref(kv), B, T, prefix_len, C.byref(b)), "hq_attn_workspace_bytes")
+    return b.value
+
+
+def hq_attn_plan(desc, kv, B, T, prefix_len) -> list:
+    """The kernel launches hq_attn would enqueue for these sizes, one string each (host only)."""
+    buf = C.create_string_buffer(4096)
+    _check(lib().hq_attn_plan(C.byref(desc), C.byref(kv), B, T, prefix_len, buf, len(buf)), "hq_attn_plan")
+    txt = buf.value.decode()
+    return txt.split(";") if txt else []
+
+
+def hq_attn(desc, kv, B, T, q, q_stride, k_cache, v_cache, prefix_table, prefix_len, block_table, max_blocks, kv_lens, cu_new,
+            out, out_stride, lse=None, workspace=None, ws_bytes=0, k_scale=None, v_scale=None, stream=None) -> None:
+    _check(lib().hq_attn(C.byref(desc), C.byref(kv), B, T, _dp(q), q_stride, _dp(k_cache), _dp(v_cache), _dp(k_scale),
+                         _dp(v_scale), _dp(prefix_table), prefix_len, _dp(block_table), max_blocks, _dp(kv_lens),
+                         _dp(cu_new), _dp(out), out_stride, _dp(lse), _dp(workspace), ws_bytes, _stream(stream)), "hq_attn")

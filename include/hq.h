@@ -15,6 +15,9 @@
  * descriptor may ask for a batch-invariant reduction order or override the
  * kernel choice (tuning); two probes measure the device's attainable peaks.
  *
+ * Around a paged key/value cache: block tables and slot maps, rotary positions
+ * with the cache write, and attention behind a prefix that requests share.
+ *
  * Sources.  The operation and its parameters follow the Humming pages:
  *  - "Humming wird angekuendigt", section "Eine einheitliche
  *    Quantisierungsdarstellung": weights, scales, zero-points and second-level
@@ -504,6 +507,173 @@ hq_status hq_moe_align(int64_t T, int32_t top_k, int32_t num_experts, const int3
  */
 hq_status hq_moe_gather(int32_t dtype, int64_t T, int32_t top_k, int64_t K, const void* A,
                         const int32_t* sorted_pairs, void* A_sorted, hq_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* paged key/value cache: slots, rotary positions, attention (device)       */
+/* ---------------------------------------------------------------------- */
+
+/*
+ * The work between a served layer's QKV projection and its output projection
+ * (both hq_gemm calls): where new tokens go in a paged cache, their rotary
+ * positions and the write, and attention over a prefix that every request
+ * shares followed by each request's own pages.
+ *
+ * Cache descriptor.  Keys and values are two buffers of num_blocks pages of
+ * block_size tokens; element (page b, token s, head h, element d) of either is
+ * at b*block_stride + s*slot_stride + h*head_stride + d (in elements, so both
+ * [page][token][head][d] and [page][head][token][d] are described, and pages
+ * may be padded).  dtype BF16 or FP16, or FP8_E4M3 with one positive fp32
+ * scale per head for keys and one for values (value = code * scale).
+ * head_dim: a multiple of 16, 16..256.  Strides: multiples of 16, at least 16,
+ * not checked against each other.  block_size 1..65536 (any integer).
+ * num_blocks * block_size below 2^31.
+ */
+typedef struct hq_kv_desc {
+    int32_t abi_version; /* HQ_ABI_VERSION                                 */
+    int32_t dtype;       /* HQ_DT_BF16, HQ_DT_FP16 or HQ_DT_FP8_E4M3        */
+    int64_t num_blocks;
+    int32_t block_size;  /* tokens of a page                                */
+    int32_t kv_heads;    /* 1..1024                                         */
+    int32_t head_dim;
+    int32_t reserved;    /* must be zero                                    */
+    int64_t block_stride, slot_stride, head_stride; /* elements            */
+} hq_kv_desc;
+
+/*
+ * Rotary positions.  Element pairs of the first rot_dim elements of a head
+ * (HALF: d and d + rot_dim/2; INTERLEAVED: 2d and 2d+1; d < rot_dim/2) turn by
+ * the angle position * f_d; the rest of the head passes through.
+ *   f_d = base^(-2d / rot_dim), stretched for contexts beyond the trained one:
+ *   NONE    as it is
+ *   LINEAR  f_d / factor
+ *   NTK     base replaced by base * factor^(rot_dim / (rot_dim - 2))
+ *   PARTS   with t_d = context * f_d / (2 pi) turns in the trained context and
+ *           g_d = clamp((t_d - slow) / (fast - slow), 0, 1):
+ *           f_d * g_d + (f_d / factor) * (1 - g_d); cos and sin are multiplied
+ *           by attn_factor (0: 0.1 ln(factor) + 1)
+ * rot_dim: a multiple of 16, 16..256.  base > 1; factor >= 1; PARTS: context
+ * >= 1 and fast > slow.  Every kind but PARTS needs attn_factor 0.
+ */
+typedef enum hq_rope_layout { HQ_ROPE_HALF = 1, HQ_ROPE_INTERLEAVED = 2 } hq_rope_layout;
+typedef enum hq_rope_scaling { HQ_ROPE_NONE = 0, HQ_ROPE_LINEAR = 1, HQ_ROPE_NTK = 2, HQ_ROPE_PARTS = 3 } hq_rope_scaling;
+typedef struct hq_rope_desc {
+    int32_t abi_version; /* HQ_ABI_VERSION                                 */
+    int32_t rot_dim;
+    int32_t layout;      /* hq_rope_layout                                  */
+    int32_t scaling;     /* hq_rope_scaling                                 */
+    double base, factor;
+    double context;      /* trained context, PARTS                          */
+    double slow, fast;   /* turns that are stretched fully / kept, PARTS    */
+    double attn_factor;
+} hq_rope_desc;
+
+/*
+ * Attention descriptor.  Token t of request r sees the shared prefix and the
+ * request's own keys up to and including its own position:
+ *   out = sum_j softmax_j(c(scale * q.k_j)) v_j,  c(x) = softcap * tanh(x / softcap)
+ *   (softcap 0: c(x) = x).
+ * q_heads: a multiple of kv_heads; query head h reads key head h / (q_heads /
+ * kv_heads).  max_new and max_kv bound every request's new tokens and own
+ * length; they and total_kv size the launch: values that are too small leave
+ * tokens or keys out, larger ones only cost idle workgroups.  total_kv is the
+ * sum of the own lengths if the caller knows it (a hint), else 0.
+ */
+typedef struct hq_attn_desc {
+    int32_t abi_version; /* HQ_ABI_VERSION                                 */
+    int32_t dtype;       /* of q and out: HQ_DT_BF16 or HQ_DT_FP16          */
+    int32_t q_heads;
+    int32_t reserved;    /* must be zero                                    */
+    int64_t max_new, max_kv, total_kv;
+    float scale;         /* finite, positive                                */
+    float softcap;       /* finite, >= 0                                    */
+} hq_attn_desc;
+
+/* Requests of one hq_kv_slots call. */
+#define HQ_KV_MAX_REQUESTS 4096
+
+/*
+ * Block tables and slot maps from request lengths.  For request r with
+ * cached_lens[r] tokens in its pages and new_lens[r] new ones, P = block_size:
+ *   cu_new [B+1]    exclusive prefix sum of new_lens
+ *   kv_lens [B]     cached + new
+ *   block_table [B][max_blocks]  entries ceil(cached/P) .. ceil((cached+new)/P)-1
+ *                   are taken from free_blocks in request order (the others
+ *                   are left as they are)
+ *   taken [1]       how many that is; if it exceeds n_free, the entries beyond
+ *                   free_blocks are written as -1
+ *   positions [T_cap], slots [T_cap]  for each new token in request order:
+ *                   first_pos + its index in the request, and table entry * P +
+ *                   index % P (-1 where the table has no page for it);
+ *                   entries past cu_new[B] become 0 and -1
+ * Negative lengths count as 0, sums saturate at 2^31-1.  All integer buffers
+ * need only their own alignment.  B == 0 writes cu_new[0] = taken[0] = 0 and
+ * the padding.  free_blocks may be NULL if n_free is 0.  The outputs must not
+ * overlap the inputs.
+ */
+hq_status hq_kv_slots(int32_t block_size, int64_t B, int64_t T_cap, int64_t max_blocks, int64_t first_pos,
+                      const int32_t* cached_lens, const int32_t* new_lens, const int32_t* free_blocks, int64_t n_free,
+                      int32_t* block_table, int32_t* cu_new, int32_t* kv_lens, int32_t* positions, int64_t* slots,
+                      int32_t* taken, hq_stream_t stream);
+
+/*
+ * Rotary table rows first_pos .. first_pos + count - 1: fp32 [count][rot_dim],
+ * cos of the rot_dim/2 angles, then their sin.  Angles are reduced in 64 bits,
+ * so no position loses accuracy.  first_pos + count <= 2^31.
+ */
+hq_status hq_rope_table(const hq_rope_desc* rope, int64_t first_pos, int64_t count, float* table, hq_stream_t stream);
+
+/*
+ * Rotates T tokens' queries and keys and writes keys and values to the cache.
+ *   q, k, v    device, dtype (BF16 or FP16); token t's row at t * stride
+ *              elements holds its heads one after the other (q_heads, kv_heads,
+ *              kv_heads rows of head_dim): three slices of one fused QKV output,
+ *              or separate buffers.  Strides: multiples of 8, at least a row
+ *   positions  int32 [T]; table: rows 0..table_rows-1 of hq_rope_table (a
+ *              position outside is clamped to the nearest row)
+ *   slots      int64 [T], page * block_size + token; outside the cache (-1):
+ *              the token's k and v are not written.  Distinct, or it is undefined
+ *              which token stays
+ *   q_out      rotated q, dtype, row stride q_out_stride; may be q itself with
+ *              the same stride
+ * fp32 arithmetic, one rounding (16-bit; E4M3 of x / scale, fp32 division,
+ * saturating at +-448, NaN kept).  Only rope->layout and rot_dim (<= head_dim)
+ * are used here.  A 16-bit cache must have q's dtype.
+ */
+hq_status hq_rope_kv(const hq_rope_desc* rope, const hq_kv_desc* kv, int32_t dtype, int64_t T, int32_t q_heads,
+                     const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                     const int32_t* positions, const float* table, int64_t table_rows, const int64_t* slots,
+                     void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache, const float* k_scale,
+                     const float* v_scale, hq_stream_t stream);
+
+/*
+ * Attention of T new tokens of B requests (cu_new, kv_lens of hq_kv_slots, the
+ * cache as hq_rope_kv left it).
+ *   q, out     device, dtype; token t's row at t * stride elements, heads one
+ *              after the other.  Strides: multiples of 8, at least a row
+ *   prefix_table, prefix_len  pages of the shared prefix, in order, and its
+ *              tokens (any number; 0 with NULL)
+ *   block_table [B][max_blocks], kv_lens [B] (own keys, new tokens included),
+ *              cu_new [B+1]
+ *   k_scale, v_scale  fp32 [kv_heads] for an E4M3 cache, else NULL
+ *   lse        fp32 [T][q_heads] or NULL: log sum_j exp(c(scale q.k_j))
+ * A token that sees no key gets out = 0 and lse = -inf.  Keys that a token does
+ * not see never reach it, whatever they hold (NaN and infinities included);
+ * bytes of the cache beyond the lengths are not read.  Pages outside the cache
+ * read as zeros.  Rows at and past cu_new[B] are not written.  Products take
+ * 16-bit operands (softmax weights rounded to dtype), sums are fp32, one rounding
+ * at the end.  The order of the sums depends on shapes and lengths only, so
+ * equal calls give equal bits.
+ */
+hq_status hq_attn_workspace_bytes(const hq_attn_desc* desc, const hq_kv_desc* kv, int64_t B, int64_t T,
+                                  int64_t prefix_len, size_t* bytes);
+hq_status hq_attn(const hq_attn_desc* desc, const hq_kv_desc* kv, int64_t B, int64_t T, const void* q, int64_t q_stride,
+                  const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                  const int32_t* prefix_table, int64_t prefix_len, const int32_t* block_table, int64_t max_blocks,
+                  const int32_t* kv_lens, const int32_t* cu_new, void* out, int64_t out_stride, float* lse,
+                  void* workspace, size_t ws_bytes, hq_stream_t stream);
+/* Host only: the launches of hq_attn for these sizes, as hq_gemm_plan names them. */
+hq_status hq_attn_plan(const hq_attn_desc* desc, const hq_kv_desc* kv, int64_t B, int64_t T, int64_t prefix_len, char* buf,
+                       size_t len);
 
 /*
  * Measurement probes (not part of the GEMM path): what the device delivers, for
