@@ -436,10 +436,8 @@ static hq_status describe_kv(const hq_kv_desc* d, KvLayout* L) {
         return set_error(HQ_ERR_UNSUPPORTED, "head_dim %d (a multiple of 16, 16..256)", d->head_dim);
     const int64_t st[3] = {d->block_stride, d->slot_stride, d->head_stride};
     for (int64_t s : st)
-        if (s < 16 || s % 16 || s > ((int64_t)1 << 40))
-            return set_error(HQ_ERR_INVALID_ARG, "cache stride %lld (a positive multiple of 16)", (long long)s);
-    if ((d->block_stride >> 8) * d->num_blocks > ((int64_t)1 << 40))
-        return set_error(HQ_ERR_UNSUPPORTED, "the cache spans more than 2^48 elements");
+        if (s < 16 || s % 16 || s > ((int64_t)1 << 31) - 16)
+            return set_error(HQ_ERR_INVALID_ARG, "cache stride %lld (a positive multiple of 16, below 2^31)", (long long)s);
     *L = KvLayout{d->block_stride, d->slot_stride, d->head_stride, d->num_blocks, d->kv_heads, d->head_dim, d->block_size,
                   FastDiv::of((uint32_t)d->block_size), d->dtype};
     return HQ_OK;

@@ -524,8 +524,8 @@ hq_status hq_moe_gather(int32_t dtype, int64_t T, int32_t top_k, int64_t K, cons
  * [page][token][head][d] and [page][head][token][d] are described, and pages
  * may be padded).  dtype BF16 or FP16, or FP8_E4M3 with one positive fp32
  * scale per head for keys and one for values (value = code * scale).
- * head_dim: a multiple of 16, 16..256.  Strides: multiples of 16, at least 16,
- * not checked against each other.  block_size 1..65536 (any integer).
+ * head_dim: a multiple of 16, 16..256.  Strides: multiples of 16, 16 to 2^31-16
+ * each, not checked against each other.  block_size 1..65536 (any integer).
  * num_blocks * block_size below 2^31.
  */
 typedef struct hq_kv_desc {
