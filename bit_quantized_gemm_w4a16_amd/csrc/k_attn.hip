@@ -28,10 +28,14 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) v4s* lds_v4s;
 typedef __attribute__((address_space(3))) v2i* lds_v2i;
+typedef __attribute__((address_space(3))) float lds_float;
+typedef __attribute__((address_space(3))) v4f lds_v4f;
 
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kCols = 32;                       // query rows of a wave's matrix tile
+constexpr int kFewTiles = 2;                    // tiles of kCols rows up to which a request counts as few rows
 constexpr int kRowsWide = kWaves * kCols;       // rows of a workgroup whose waves take different rows
+constexpr int kMaxParts = 256;                  // of the prefix, and of a request's own keys (the join keeps their weights in LDS)
 constexpr int kAll = 0x7FFFFFFF;               // lim0: every row sees every key
 constexpr float kNone = -3.0e38f;               // running maximum before any key
 constexpr float kSlack = 8.f;                   // weights stay below 2^kSlack
@@ -40,15 +44,16 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // How a call is cut into workgroups.  Three kinds of work in one launch:
 // prefix (all rows of a key head, the shared keys), few (a request with at most
 // kCols rows per key head: the four waves take different keys of each tile and
-// are joined at the end) and many (a request with more rows: the waves take
-// different rows).  `joint`: a request's workgroups walk the prefix themselves.
+// are joined at the end; up to kFewTiles such tiles of one request) and many (a
+// request with more rows: the waves take different rows).  `joint`: a request's workgroups walk the prefix themselves.
 struct Plan {
     int pre_tiles, pre_parts, pre_chunk;
-    bool pre_few;                    // the prefix rows fit one wave's tile
-    int few_parts, few_chunk;
+    bool pre_few;                    // the rows at the prefix count as few
+    int few_parts, few_chunk, few_tiles;
     int many_tiles, many_parts, many_chunk;
     bool joint;
-    int64_t pre_units, few_units, many_units;
+    uint32_t pre_units, few_units, many_units;  // (make_plan checks their sum before it narrows them)
+    FastDiv by_heads, by_pre_tiles, by_few_parts, by_many_tiles;
     int own_parts;                   // partial results of a row from its own keys, at most
     int parts;                       // all partial results of a row; 1: written directly
 };
@@ -160,6 +165,16 @@ __device__ __forceinline__ v2u tr16(lds_char* p) { return __builtin_bit_cast(v2u
 __device__ __forceinline__ v2u tr8(lds_char* p) { return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i)p)); }
 #endif
 
+// v of lane ^ 32, without a trip through LDS.
+__device__ __forceinline__ float other_half(float v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const v2u r = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+    return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+#else
+    return v;
+#endif
+}
+
 // Waits for loads into LDS, which the compiler does not follow to their readers:
 // until at most N vector loads of this wave are open; until its LDS reads are done.
 template <int N>
@@ -191,8 +206,7 @@ struct Rows {
     float c1, c2;
     bool cap;
     int half, col, lane;
-    int64_t tok;
-    int head, seen, wseen;  // keys that this lane's row sees; that every row of the wave sees
+    int seen, wseen;  // keys that this lane's row sees; that every row of the wave sees
     bool live;
 
     // s = c2 x.k, or with a cap s = c2 tanh(y), tanh(y) = 1 - 2 / (1 + 2^(c1 x.k))
@@ -205,8 +219,8 @@ struct Rows {
         const int row = wrow0 + col;
         live = row < nrows;
         const int rtok = live ? (int)ka.per_group.div(row) : 0;
-        tok = tok0 + rtok;
-        head = kvh * ka.G + (live ? row - rtok * ka.G : 0);
+        const int64_t tok = tok0 + rtok;
+        const int head = kvh * ka.G + (live ? row - rtok * ka.G : 0);
         const int wtok = (int)ka.per_group.div(wrow0 < nrows ? wrow0 : 0);
         seen = min(k1, lim0 == kAll ? k1 : max(keys.shared, lim0 + rtok));
         wseen = __builtin_amdgcn_readfirstlane(min(k1, lim0 == kAll ? k1 : max(keys.shared, lim0 + wtok)));
@@ -259,7 +273,7 @@ struct Rows {
         float mx = st[0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) mx = fmaxf(mx, st[i]);
-        mx = fmaxf(mx, __shfl_xor(mx, 32)) * c2;
+        mx = fmaxf(mx, other_half(mx)) * c2;
         // The maximum that the weights are taken against only has to keep them in
         // range: it moves, and the sums with it, once it is behind by 2^kSlack.
         if (__any(mx > m + kSlack)) {
@@ -362,38 +376,39 @@ struct Rows {
                 }
         }
     }
-    // The rows' result, or their partial one: (m, l, sum of weight times value).
-    __device__ __forceinline__ void store(const KArgs& ka, int kvh, int part, bool direct) {
-        const AttnArgs& a = ka.a;
-        const int D = a.kv.head_dim;
+    // The sums of this wave's rows into LDS, as rows of kPitch floats (padded, so
+    // that eight rows meet in no bank).
+    static constexpr int kPitch = DP + 4;
+    __device__ __forceinline__ void spill(lds_float* o) {
         if (!live) return;
-        const float vsc = FP8 ? a.v_scale[kvh] : 1.f;
-        const int64_t pr = ((int64_t)part * a.T + tok) * a.q_heads + head;
-        const float f = !direct ? vsc : l > 0.f || l != l ? vsc / l : 0.f;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int d = 32 * t + 8 * g + 4 * half;
-                if (d >= D) continue;
-                v4f o;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = acc[t][4 * g + j] * f;
-                if (direct)
-                    *(uint2*)((uint16_t*)a.out + tok * a.out_stride + (int64_t)head * D + d) = make_uint2(pack2<BF16>(o[0], o[1]), pack2<BF16>(o[2], o[3]));
-                else
-                    *(v4f*)(ka.part_o + pr * D + d) = o;
-            }
-        if (half == 0) {
-            if (!direct) {
-                ka.part_m[pr] = m;
-                ka.part_l[pr] = l;
-            } else if (a.lse) {
-                a.lse[tok * a.q_heads + head] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
-            }
-        }
+            for (int g = 0; g < 4; ++g)
+                *(lds_v4f*)(o + col * kPitch + 32 * t + 8 * g + 4 * half) = v4f{acc[t][4 * g], acc[t][4 * g + 1], acc[t][4 * g + 2], acc[t][4 * g + 3]};
     }
 };
+
+// Four elements of a row's result, or of its partial one (m, l and the sum of
+// weight times value), to where they belong.
+template <bool BF16, bool FP8>
+__device__ __forceinline__ void put(const KArgs& ka, int kvh, int64_t tok0, int row, int d, v4f o, float m, float l, int part, bool direct) {
+    const AttnArgs& a = ka.a;
+    const int D = a.kv.head_dim, rt = (int)ka.per_group.div(row), head = kvh * ka.G + row - rt * ka.G;
+    const int64_t tok = tok0 + rt, at = tok * a.q_heads + head;
+    float f = FP8 ? a.v_scale[kvh] : 1.f;
+    if (direct) {
+        f = l > 0.f || l != l ? f / l : 0.f;
+        *(uint2*)((uint16_t*)a.out + tok * a.out_stride + (int64_t)head * D + d) = make_uint2(pack2<BF16>(o[0] * f, o[1] * f), pack2<BF16>(o[2] * f, o[3] * f));
+        if (d == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    } else {
+        *(v4f*)(ka.part_o + ((int64_t)part * a.T * a.q_heads + at) * D + d) = o * f;
+        if (d == 0) {  // a row's parts side by side
+            ka.part_m[at * ka.p.parts + part] = m;
+            ka.part_l[at * ka.p.parts + part] = l;
+        }
+    }
+}
 
 // What a workgroup does.
 struct Task {
@@ -410,6 +425,12 @@ struct Task {
 // Zeros for what is loaded into LDS in place of keys that do not exist.
 __device__ __attribute__((aligned(16))) const uint32_t g_zeros[4] = {0, 0, 0, 0};
 
+// Groups of 32 keys that a wave has room for.  16-bit rows fill the LDS of two
+// workgroups a CU with one; with half the bytes of an 8-bit cache a second one
+// keeps as many bytes on their way.
+template <bool FP8>
+constexpr int kStages = FP8 ? 2 : 1;
+
 // At most 32 rows.  The cache is read once, so what bounds this is HBM: each
 // wave takes every fourth group of 32 keys by itself, with no barrier, straight
 // from memory into its own LDS tiles.  The tile of K is free once the scores are
@@ -422,31 +443,31 @@ __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_c
     constexpr int EB = FP8 ? 1 : 2, B = DP * EB;   // bytes of a row
     constexpr int LPR = B / 16, RPL = 64 / LPR;    // lanes of a row, rows of a load
     constexpr int NL = 32 / RPL;
+    constexpr int NS = kStages<FP8>, TILE = 32 * B;
     const KvLayout& kv = ka.a.kv;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Rows<DP, BF16, FP8> x;
     x.init(ka, w.keys, w.kvh, w.tok0, w.nrows, w.row0, w.k1, w.lim0);
-    lds_char* lk = sk + wave * 32 * B;
-    lds_char* lv = sv + wave * 32 * B;
+    lds_char* const wk = sk + wave * NS * TILE;  // this wave's tiles
+    lds_char* const wv = sv + wave * NS * TILE;
     const char* kb0 = (const char*)ka.a.k_cache + (int64_t)w.kvh * kv.head_stride * EB;
     const char* vb0 = (const char*)ka.a.v_cache + (int64_t)w.kvh * kv.head_stride * EB;
     const uint32_t bstep = (uint32_t)(kv.block_stride * EB), sstep = (uint32_t)(kv.slot_stride * EB);
-    const int row_bytes = kv.head_dim * EB;
+    const int D = kv.head_dim, row_bytes = D * EB;
     int32_t pid;
     uint32_t pat;
+    bool key = false;  // was the row that was looked up a key
     auto look = [&](int kb) {
-        const int i = kb + x.col;
-        pid = -1;
-        pat = 0;
-        if (i < w.k1) pid = w.keys.page(kv, i, pat);
+        key = kb + x.col < w.k1;
+        pid = w.keys.page(kv, min(kb + x.col, w.k1 - 1), pat);
     };
     // byte offset of this lane's key in the cache, -1 if there is none
-    int64_t koff, voff;
+    int64_t off = -1;
     auto offset = [&]() {
-        const bool ok = (uint32_t)pid < (uint32_t)kv.num_blocks;
+        const bool ok = key && (uint32_t)pid < (uint32_t)kv.num_blocks;
         return ok ? (int64_t)((uint64_t)(uint32_t)pid * bstep + (uint64_t)pat * sstep) : (int64_t)-1;
     };
-    auto fetch = [&](const char* base, int64_t off, lds_char* to) {
+    auto fetch = [&](const char* base, lds_char* to) {
 #if defined(__HIP_DEVICE_COMPILE__)
         const uint32_t lo = (uint32_t)off, hi = (uint32_t)((uint64_t)off >> 32);
 #pragma unroll
@@ -462,19 +483,27 @@ __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_c
     constexpr int STEP = kWaves * 32;
     int kb = w.k0 + wave * 32;
     bool bad = false;
-    if (kb < w.k1) {
+    if (w.k0 < w.k1) {
         look(kb);
-        koff = voff = offset();
-        fetch(kb0, koff, lk);
-        fetch(vb0, voff, lv);
-        look(kb + STEP);
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            if (kb + n * STEP < w.k1) {
+                off = offset();
+                fetch(kb0, wk + n * TILE);
+                fetch(vb0, wv + n * TILE);
+            }
+            look(kb + (n + 1) * STEP);
+        }
     }
     x.ready();
+    lds_char *lk = wk, *lv = wv;
     for (; kb < w.k1; kb += STEP) {
-        const bool more = kb + STEP < w.k1;
-        // Loads end in order.  After K of this group came at least V of it (and at
-        // most one page id); after V, if there is a next group, its K.
-        wait_loads<NL>();
+        const bool next = kb + STEP < w.k1, more = kb + NS * STEP < w.k1;
+        // Loads end in order, and K and V of a group are NL each.  After K of this
+        // group came its V, and K and V of the groups that are already asked for
+        // (and page ids, which can only make these waits longer).
+        if (NS == 2 && next) wait_loads<3 * NL>();
+        else wait_loads<NL>();
         v16f st;
 #pragma unroll
         for (int i = 0; i < 16; ++i) st[i] = 0.f;
@@ -494,15 +523,17 @@ __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_c
             st = mfma32<BF16>(f1, x.q[2 * g + 1], st);
         }
         if (more) {
-            koff = offset();
+            off = offset();
             wait_lds();  // the tile of K has been read
-            fetch(kb0, koff, lk);
-            look(kb + 2 * STEP);
+            fetch(kb0, lk);
+            look(kb + (NS + 1) * STEP);
         }
         x.prepare(st, kb);
         Frag8 p[2];
         x.weights(st, p);
-        if (more) wait_loads<NL>();
+        // after V of this group: K and V of the next, K of the one after
+        if (more) wait_loads<(2 * NS - 1) * NL>();
+        else if (NS == 2 && next) wait_loads<2 * NL>();
         else wait_loads<0>();
         if (min(kb + 32, w.k1) > x.wseen) {  // some row does not see some of these keys
 #pragma unroll 1
@@ -516,49 +547,45 @@ __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_c
         x.values_dense(lv, p);
         if (more) {
             wait_lds();  // the tile of V has been read
-            fetch(vb0, koff, lv);
+            fetch(vb0, lv);
+        }
+        if constexpr (NS == 2) {
+            lk = lk == wk ? wk + TILE : wk;
+            lv = lv == wv ? wv + TILE : wv;
         }
     }
-    x.l += __shfl_xor(x.l, 32);
+    x.l += other_half(x.l);
     if (__any(bad)) x.add_nonfinite(ka, w.keys, w.kvh, x.wseen < w.k0 ? w.k0 : w.k0 + (x.wseen - w.k0) / 32 * 32, w.k0, w.k1, kWaves, wave);
 
-    // Joining: waves 2 and 3 into 0 and 1, then 1 into 0.  A lane meets its own
-    // counterpart, so the layout is the registers'.
-    auto lo = (__attribute__((address_space(3))) float*)sk;
-    typedef __attribute__((address_space(3))) v4f lds_v4f;
-    constexpr int PER = (DP / 32 * 16 + 2) * 64;  // floats of a wave
-#pragma unroll
-    for (int n = 2; n >= 1; n >>= 1) {
-        __syncthreads();
-        if (wave >= n && wave < 2 * n) {
-            auto o = lo + (wave - n) * PER;
-            o[x.lane] = x.m;
-            o[64 + x.lane] = x.l;
-#pragma unroll
-            for (int t = 0; t < DP / 32; ++t)
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    *(lds_v4f*)(o + 128 + ((t * 4 + g) * 64 + x.lane) * 4) =
-                        v4f{x.acc[t][4 * g], x.acc[t][4 * g + 1], x.acc[t][4 * g + 2], x.acc[t][4 * g + 3]};
-        }
-        __syncthreads();
-        if (wave < n) {
-            auto o = lo + wave * PER;
-            const float m2 = o[x.lane], to = fmaxf(x.m, m2);
-            const float f1 = __builtin_amdgcn_exp2f(x.m - to), f2 = __builtin_amdgcn_exp2f(m2 - to);
-            x.m = to;
-            x.l = x.l * f1 + o[64 + x.lane] * f2;
-#pragma unroll
-            for (int t = 0; t < DP / 32; ++t)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const v4f y = *(const lds_v4f*)(o + 128 + ((t * 4 + g) * 64 + x.lane) * 4);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x.acc[t][4 * g + j] = x.acc[t][4 * g + j] * f1 + y[j] * f2;
-                }
-        }
+    // The waves' results meet in LDS, and all threads join them, four elements at
+    // a time (in a loop, and only the rows there are: with few keys a workgroup's
+    // time is the latency of code that it runs once).
+    typedef Rows<DP, BF16, FP8> R;
+    __shared__ float s_m[kWaves][kCols], s_l[kWaves][kCols];
+    if (x.half == 0) {
+        s_m[wave][x.col] = x.m;
+        s_l[wave][x.col] = x.l;
     }
-    if (wave == 0) x.store(ka, w.kvh, w.part, w.direct);
+    __syncthreads();
+    x.spill((lds_float*)(wave < 2 ? sk : sv) + (wave & 1) * kCols * R::kPitch);
+    __syncthreads();
+    const int rows = min(kCols, w.nrows - w.row0);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < rows * (DP / 4); i += kThreads) {
+        const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+        if (d >= D) continue;
+        float m = s_m[0][r], l = 0.f;
+#pragma unroll
+        for (int v = 1; v < kWaves; ++v) m = fmaxf(m, s_m[v][r]);
+        v4f o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+            const float f = __builtin_amdgcn_exp2f(s_m[v][r] - m);
+            l += f * s_l[v][r];
+            o += f * *(const lds_v4f*)((lds_float*)(v < 2 ? sk : sv) + ((v & 1) * kCols + r) * R::kPitch + d);
+        }
+        put<BF16, FP8>(ka, w.kvh, w.tok0, w.row0 + r, d, o, m, l, w.part, w.direct);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -568,13 +595,13 @@ __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_c
 // Each wave has 32 rows of its own; tiles of 64 keys are staged in LDS for all
 // four, in two buffers.  What bounds this is the matrix units and, with as many
 // cycles, the exponentials, so a wave starts the score product of the next 32
-// keys before it turns the last ones into weights.  K and V of the next tile
-// travel one after the other, through the same registers.
+// keys before it turns the last ones into weights.  K and V come through
+// registers and are asked for one whole tile before they are staged.
 template <int DP, bool BF16, bool FP8>
 __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_char* sk, lds_char* sv) {
     constexpr int KT = 64;
     constexpr int EPC = FP8 ? 16 : 8, EB = FP8 ? 1 : 2;
-    constexpr int NL = DP / 4 / EPC;        // 16-byte loads of a thread: a quarter of a row
+    constexpr int NL = DP / 4 / EPC;  // 16-byte loads of a thread: a quarter of a row
     constexpr int KP = Padded<DP>::K, VP = Padded<DP>::V;
     typedef __attribute__((address_space(3))) v4u lds_v4u;
     const KvLayout& kv = ka.a.kv;
@@ -592,27 +619,27 @@ __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_
     const char* kb0 = (const char*)ka.a.k_cache + (int64_t)w.kvh * kv.head_stride * EB;
     const char* vb0 = (const char*)ka.a.v_cache + (int64_t)w.kvh * kv.head_stride * EB;
     const uint32_t bstep = (uint32_t)(kv.block_stride * EB), sstep = (uint32_t)(kv.slot_stride * EB);
-    v4u rg[NL];
+    v4u rk[NL], rv[NL];
     int32_t pid = -1;
     uint32_t pat = 0;
-    uint64_t off = 0;
-    bool ok = false;
+    bool key = false;              // was the row that was looked up a key
+    uint64_t off = 0;              // of the row that is being loaded
+    bool ok = false, okn = false;  // is there a key: in the tile that is staged next, in the one that is loaded
     auto look = [&](int kt) {
-        const int i = kt + sr;
-        pid = -1;
-        if (i < w.k1) pid = w.keys.page(kv, i, pat);
-    };
-    auto settle = [&]() {  // the offset of the row that was looked up
-        ok = (uint32_t)pid < (uint32_t)kv.num_blocks;
-        off = (uint64_t)(ok ? (uint32_t)pid : 0u) * bstep + (uint64_t)(ok ? pat : 0u) * sstep;
+        key = kt + sr < w.k1;
+        pid = w.keys.page(kv, min(kt + sr, w.k1 - 1), pat);
     };
     // What is no key of this workgroup, or beyond the head, reads the cache's first
     // elements instead and is zeroed before use: no load hides behind a branch.
-    auto load = [&](const char* base) {
+    auto settle = [&]() {  // the row that was looked up is the next to load
+        okn = key && (uint32_t)pid < (uint32_t)kv.num_blocks;
+        off = (uint64_t)(okn ? (uint32_t)pid : 0u) * bstep + (uint64_t)(okn ? pat : 0u) * sstep;
+    };
+    auto load = [&](const char* base, v4u (&rg)[NL]) {
 #pragma unroll
         for (int n = 0; n < NL; ++n) rg[n] = ld16(base + off + ((4 * n + sc) * EPC < D ? (4 * n + sc) * 16 : 0));
     };
-    auto stage = [&](lds_char* to) {  // to: this thread's place in its row
+    auto stage = [&](lds_char* to, v4u (&rg)[NL]) {  // to: this thread's place in its row
         if (D < DP || !__all(ok)) {
 #pragma unroll
             for (int n = 0; n < NL; ++n) rg[n] &= ok && (4 * n + sc) * EPC < D ? ~0u : 0u;
@@ -632,12 +659,12 @@ __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_
         if (min(kt + KT, w.k1) > gseen) {  // some row does not see some of these keys
 #pragma unroll
             for (int n = 0; n < NL; ++n) {
-                const v4u f = finite_of<BF16, FP8>(rg[n]);
-                bad |= ok && differ(f, rg[n]);
-                rg[n] = f;
+                const v4u f = finite_of<BF16, FP8>(rv[n]);
+                bad |= ok && differ(f, rv[n]);
+                rv[n] = f;
             }
         }
-        stage(to);
+        stage(to, rv);
     };
     auto scores = [&](lds_char* k, v16f& st) {  // k: this lane's row and half
 #pragma unroll
@@ -654,32 +681,39 @@ __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_
     lds_char* const get_k = sk + x.col * KP + 32 * x.half;
     v16f s0, s1;
     Frag8 p[2];
-    if (w.k0 < w.k1) look(w.k0);
+    if (w.k0 < w.k1) {
+        look(w.k0);
+        settle();
+        load(kb0, rk);
+        load(vb0, rv);
+        ok = okn;
+        look(w.k0 + KT);
+    }
     x.ready();
     if (w.k0 < w.k1) {
+        stage(put_k, rk);
         settle();
-        load(kb0);
-        stage(put_k);
-        load(vb0);
-        look(w.k0 + KT);
+        load(kb0, rk);
+        look(w.k0 + 2 * KT);
         stage_v(w.k0, put_v);
-        settle();
-        load(kb0);
+        load(vb0, rv);
+        ok = okn;
         __syncthreads();
         if (wlive) {
             scores(get_k, s0);
             x.prepare(s0, w.k0);
         }
     }
-    // Tile kt from one buffer while tile kt + 64 comes into the other.  On entry:
-    // the scores of its first 32 keys, and K of the next tile in registers.
+    // Tile kt from one buffer while tile kt + 64 goes into the other.  On entry:
+    // the scores of its first 32 keys, and the next tile in registers.  The loads
+    // are the same on every way through, at the end of nothing but zeros to be, so
+    // that each is waited for by its place in the queue.
     auto step = [&](int kt, int kc, int vc, int kn, int vn) {
         const bool more = kt + KT < w.k1;
-        if (more) {
-            stage(put_k + kn);
-            load(vb0);
-            look(kt + 2 * KT);
-        }
+        stage(put_k + kn, rk);
+        settle();
+        load(kb0, rk);
+        look(kt + 3 * KT);
         if (wlive) {
             scores(get_k + kc + 32 * KP, s1);
             x.weights(s0, p);
@@ -687,11 +721,9 @@ __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_
             x.prepare(s1, kt + 32);
         }
         __syncthreads();  // K of the next tile is there
-        if (more) {
-            stage_v(kt + KT, put_v + vn);
-            settle();
-            load(kb0);
-        }
+        stage_v(kt + KT, put_v + vn);
+        load(vb0, rv);
+        ok = okn;
         if (wlive) {
             if (more) scores(get_k + kn, s0);
             x.weights(s1, p);
@@ -704,24 +736,54 @@ __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_
         step(kt, 0, 0, KT * KP, KT * VP);
         if (kt + KT < w.k1) step(kt + KT, KT * KP, KT * VP, 0, 0);
     }
-    x.l += __shfl_xor(x.l, 32);
+    x.l += other_half(x.l);
     if (__syncthreads_or(bad) && wlive) x.add_nonfinite(ka, w.keys, w.kvh, gseen < w.k0 ? w.k0 : w.k0 + (gseen - w.k0) / KT * KT, w.k0, w.k1, 1, 0);
-    x.store(ka, w.kvh, w.part, w.direct);
+    // each wave's rows through its own share of the tiles' LDS, so that whole rows are written
+    typedef Rows<DP, BF16, FP8> R;
+    __shared__ float s_m[kWaves][kCols], s_l[kWaves][kCols];
+    if (x.half == 0) {
+        s_m[wave][x.col] = x.m;
+        s_l[wave][x.col] = x.l;
+    }
+    auto o = (lds_float*)(wave < 2 ? sk : sv) + (wave & 1) * kCols * R::kPitch;
+    x.spill(o);
+    __syncthreads();
+    const int rows = min(kCols, w.nrows - wrow0);
+#pragma unroll 4
+    for (int i = x.lane; i < rows * (DP / 4); i += 64) {
+        const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+        if (d < D) put<BF16, FP8>(ka, w.kvh, w.tok0, wrow0 + r, d, *(const lds_v4f*)(o + r * R::kPitch + d), s_m[wave][r], s_l[wave][r], w.part, w.direct);
+    }
 }
 
 // A unit of a segment whose workgroups come in groups of `tiles` that read the
 // same keys: whole groups go to one XCD (workgroup ids alternate between the 8
 // XCDs), so that the group's keys are fetched into one L2 only.
-__device__ __forceinline__ bool grouped_unit(int64_t id, int64_t groups, int tiles, int64_t& group, int& tile) {
-    if (groups % 8 == 0 || groups >= 32) {
-        const int64_t j = id >> 3;
-        group = (j / tiles) * 8 + (id & 7);
-        tile = (int)(j % tiles);
-        return group < groups;
+__device__ __forceinline__ bool grouped_unit(uint32_t id, uint32_t groups, FastDiv tiles, uint32_t& group, int& tile) {
+    const bool spread = groups % 8 == 0 || groups >= 32;
+    const uint32_t j = spread ? id >> 3 : id, g = tiles.div(j);
+    tile = (int)(j - g * tiles.d);
+    group = spread ? g * 8 + (id & 7) : g;
+    return group < groups;
+}
+
+__device__ __forceinline__ int first_tile(const int32_t* cu, int r, int G, int T) {
+    const int t = min(max(cu[r], 0), T);
+    return (int)((int64_t)t * G / kRowsWide) + r;
+}
+// The request that owns a tile: the last r whose first tile is not beyond it.
+// The lanes of a wave look at 64 requests at a time.
+__device__ __forceinline__ int find_request(const int32_t* cu, int B, int tile, int G, int T) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = B;  // among requests lo .. lo + n - 1, lo's first tile is not beyond
+    while (n > 1) {
+        const int step = (n + 63) / 64, r = lo + lane * step;
+        const uint64_t hit = __ballot(lane * step < n && first_tile(cu, r < B ? r : B - 1, G, T) <= tile);
+        const int k = hit ? 63 - __builtin_clzll(hit) : 0;
+        n = min(step, n - k * step);
+        lo += k * step;
     }
-    group = id / tiles;
-    tile = (int)(id % tiles);
-    return true;
+    return __builtin_amdgcn_readfirstlane(lo);
 }
 
 template <int DP, bool BF16, bool FP8>
@@ -730,22 +792,22 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(KArgs
     __shared__ __attribute__((aligned(16))) char s_k[2 * 64 * Padded<DP>::K], s_v[2 * 64 * Padded<DP>::V];
     const AttnArgs& a = ka.a;
     const Plan& p = ka.p;
-    int64_t id = blockIdx.x;
+    uint32_t id = blockIdx.x;
     const bool direct = p.parts == 1;
-    const int heads = a.kv.kv_heads;
+    const uint32_t heads = a.kv.kv_heads;
     bool few;
     int kvh, part, base, row0, rows, k1, lim0;
     int64_t tok0, k0;
     Keys keys{a.prefix_table, nullptr, (int)a.prefix_len};
     if (id < p.pre_units) {
-        int64_t group;
+        uint32_t group;
         int tile;
-        if (!grouped_unit(id, (int64_t)heads * p.pre_parts, p.pre_tiles, group, tile)) return;
+        if (!grouped_unit(id, heads * p.pre_parts, p.by_pre_tiles, group, tile)) return;
         few = p.pre_few;
-        kvh = (int)(group % heads);
-        part = (int)(group / heads);
+        part = (int)p.by_heads.div(group);
+        kvh = (int)(group - part * heads);
         base = 0;
-        row0 = tile * kRowsWide;
+        row0 = tile * (few ? kCols : kRowsWide);
         rows = (int)a.T * ka.G;
         tok0 = 0;
         k0 = (int64_t)part * p.pre_chunk;
@@ -755,19 +817,25 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(KArgs
         id -= p.pre_units;
         few = id < p.few_units;
         int r, tile = 0;
-        if (few) {
-            part = (int)(id % p.few_parts);
-            const int64_t g = id / p.few_parts;
-            kvh = (int)(g % heads);
-            r = (int)(g / heads);
+        if (few) {  // heads side by side: together they read whole pages
+            uint32_t g = p.by_heads.div(id);
+            kvh = (int)(id - g * heads);
+            if (p.few_tiles > 1) {
+                tile = g % kFewTiles;
+                g /= kFewTiles;
+            }
+            r = (int)p.by_few_parts.div(g);
+            part = (int)(g - r * p.few_parts);
         } else {
-            int64_t group;
-            if (!grouped_unit(id - p.few_units, a.B * heads * p.many_parts, p.many_tiles, group, tile)) return;
-            tile = p.many_tiles - 1 - tile;  // the last rows see the most keys: first
-            part = (int)(group % p.many_parts);
-            group /= p.many_parts;
-            kvh = (int)(group % heads);
-            r = (int)(group / heads);
+            uint32_t group;
+            if (!grouped_unit(id - p.few_units, heads * p.many_parts, p.by_many_tiles, group, tile)) return;
+            part = (int)p.by_heads.div(group);
+            kvh = (int)(group - part * heads);
+            // The last tiles see the most keys: first.  Request r's tiles begin at
+            // floor(cu[r] G / kRowsWide) + r, which leaves each at least what it needs.
+            tile = p.many_tiles - 1 - tile;
+            r = find_request(a.cu, (int)a.B, tile, ka.G, (int)a.T);
+            tile -= first_tile(a.cu, r, ka.G, (int)a.T);
         }
         int64_t t0 = a.cu[r], t1 = a.cu[r + 1];
         t0 = t0 < 0 ? 0 : t0;
@@ -775,8 +843,8 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(KArgs
         const int n = t1 > t0 ? (int)min(t1 - t0, a.max_new) : 0;
         tok0 = t0;
         rows = n * ka.G;
-        row0 = tile * kRowsWide;
-        if (few != (rows <= kCols) || row0 >= rows) return;
+        row0 = tile * (few ? kCols : kRowsWide);
+        if (few != (rows <= kFewTiles * kCols) || row0 >= rows) return;
         int64_t len = a.kv_lens[r];
         len = len < 0 ? 0 : min(min(len, a.max_kv), a.max_blocks * a.kv.block_size);
         keys.own = a.block_table + (int64_t)r * a.max_blocks;
@@ -801,37 +869,68 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(KArgs
     else attend_many<DP, BF16, FP8>(ka, w, (lds_char*)s_k, (lds_char*)s_v);
 }
 
-// Joins the parts of every row: D / 4 threads a row.
+// Joins the parts of every row.  A workgroup takes `rpw` rows; the weights of
+// their parts come first, into LDS, and then D / 4 threads a row add four
+// elements each, `spl` times side by side over every spl-th part.
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(KArgs ka) {
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(KArgs ka, int rpw, int spl) {
+    extern __shared__ __attribute__((aligned(16))) float s_w[];  // [rpw][parts] weights, then [spl][rpw][D] sums
+    __shared__ float s_l[kThreads], s_m[kThreads];
     const AttnArgs& a = ka.a;
-    const int D = a.kv.head_dim, tpr = D / 4, rpw = kThreads / tpr;
-    const int sub = threadIdx.x / tpr, d4 = threadIdx.x % tpr;
-    const int64_t row = (int64_t)blockIdx.x * rpw + sub, rows = a.T * a.q_heads;
-    if (sub >= rpw || row >= rows) return;
-    const int64_t tok = row / a.q_heads;
-    if (tok >= a.cu[a.B]) return;
-    int own = ka.part_n[tok];
-    own = own < 0 ? 0 : own > ka.p.own_parts ? ka.p.own_parts : own;
-    const int n = ka.p.pre_parts + own;
-    float mm = kNone;
-    for (int p = 0; p < n; ++p) mm = fmaxf(mm, ka.part_m[(int64_t)p * rows + row]);
-    float ll = 0.f;
+    const int D = a.kv.head_dim, parts = ka.p.parts, tid = threadIdx.x;
+    const int64_t row0 = (int64_t)blockIdx.x * rpw, rows = a.T * a.q_heads, end = a.cu[a.B];
+    auto parts_of = [&](int64_t row) {
+        const int64_t tok = row / a.q_heads;
+        if (row >= rows || tok >= end) return 0;
+        const int own = ka.part_n[tok];
+        return ka.p.pre_parts + (own < 0 ? 0 : own > ka.p.own_parts ? ka.p.own_parts : own);
+    };
+    {
+        // lanes 0 .. g-1 of a group of g threads: one row's parts
+        const int g = kThreads / rpw < 64 ? kThreads / rpw : 64;
+        const int sub = tid / g, i0 = tid % g;
+        const int64_t row = row0 + sub;
+        const int n = sub < rpw ? parts_of(row) : 0;
+        float m = kNone, l = 0.f;
+        for (int p = i0; p < n; p += g) m = fmaxf(m, ka.part_m[row * parts + p]);
+        for (int o = g / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+        for (int p = i0; p < n; p += g) {
+            const float f = __builtin_amdgcn_exp2f(ka.part_m[row * parts + p] - m);
+            s_w[sub * parts + p] = f;
+            l += f * ka.part_l[row * parts + p];
+        }
+        for (int o = g / 2; o; o >>= 1) l += __shfl_xor(l, o);
+        if (i0 == 0 && sub < rpw) {
+            s_m[sub] = m;
+            s_l[sub] = l;
+        }
+    }
+    __syncthreads();
+    const int tpr = D / 4, d4 = tid % tpr, sub = tid / tpr % rpw, s = tid / tpr / rpw;
+    const int64_t row = row0 + sub;
+    const int n = s < spl ? parts_of(row) : 0;
     v4f o = {0.f, 0.f, 0.f, 0.f};
-    for (int p = 0; p < n; ++p) {
-        const int64_t at = (int64_t)p * rows + row;
-        const float f = __builtin_amdgcn_exp2f(ka.part_m[at] - mm);
-        ll += f * ka.part_l[at];
-        const v4f x = *(const v4f*)(ka.part_o + at * D + 4 * d4);
+    const float* src = ka.part_o + row * D + 4 * d4;
+    const int64_t step = rows * D;
+#pragma unroll 8
+    for (int p = s; p < n; p += spl) {
+        const v4f x = *(const v4f*)(src + p * step);
+        const float f = s_w[sub * parts + p];
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] += f * x[j];
     }
-    const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
-    const int64_t hd = row - tok * a.q_heads;
-    const uint32_t w0 = pack2<BF16>(o[0] * inv, o[1] * inv);
-    const uint32_t w1 = pack2<BF16>(o[2] * inv, o[3] * inv);
-    *(uint2*)((uint16_t*)a.out + tok * a.out_stride + hd * D + 4 * d4) = make_uint2(w0, w1);
-    if (a.lse && d4 == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+    if (spl > 1) {
+        __syncthreads();
+        if (s < spl) *(v4f*)(s_w + ((s * rpw + sub) * tpr + d4) * 4) = o;
+        __syncthreads();
+        if (s) return;
+        for (int k = 1; k < spl; ++k) o += *(const v4f*)(s_w + ((k * rpw + sub) * tpr + d4) * 4);
+    }
+    const int64_t tok = row / a.q_heads, hd = row - tok * a.q_heads;
+    if (s || row >= rows || tok >= end) return;
+    const float l = s_l[sub], inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    *(uint2*)((uint16_t*)a.out + tok * a.out_stride + hd * D + 4 * d4) = make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
+    if (a.lse && d4 == 0) a.lse[row] = l == 0.f ? -INFINITY : (s_m[sub] + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------
@@ -840,62 +939,92 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KArgs ka) {
 
 static int pad_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-static Plan make_plan(const AttnArgs& a) {
-    Plan p{};
-    const int64_t hk = a.kv.kv_heads, G = a.q_heads / hk;
+static int64_t group_units(int64_t groups, int64_t tiles) {  // grouped_unit's ids
+    return (groups % 8 == 0 || groups >= 32 ? cdiv(groups, 8) * 8 : groups) * tiles;
+}
+
+// Returns the number of workgroups, or -1 if a launch does not hold them.
+static int64_t make_plan(const AttnArgs& a, Plan& p) {
+    p = Plan{};
+    const int64_t hk = a.kv.kv_heads, G = a.q_heads / hk, P = a.prefix_len;
     const int64_t rows = a.T * G;
     const int64_t slots = pad_dim(a.kv.head_dim) == 256 ? 256 : 512;  // workgroups that run at once
-    const int64_t own = a.total_kv > 0 ? a.total_kv : a.B * a.max_kv;
-    const int64_t P = a.prefix_len;
-    const bool many = a.max_new * G > kCols;
-    // a request whose rows fill tiles by themselves gains nothing from sharing,
-    // nor does a prefix that is short beside the own keys
-    p.joint = P > 0 && (a.B == 1 || rows >= a.B * kRowsWide || P * (a.B - 1) <= own / 4);
-    const int64_t extra = p.joint ? P : 0;
-    const int64_t pre_keys = p.joint ? 0 : P;
-    if (pre_keys) {
-        p.pre_few = rows <= kCols;
-        p.pre_tiles = p.pre_few ? 1 : (int)cdiv(rows, kRowsWide);
-    }
-    // keys of a workgroup so that the card is filled about once
+    const int64_t total = a.total_kv > 0 ? a.total_kv : a.B * a.max_kv;
+    const int64_t bytes = a.kv.dtype == HQ_DT_FP8_E4M3 ? 1 : 2;
+    const bool many = a.max_new * G > kFewTiles * kCols;
     const int64_t own_tiles = many ? cdiv(rows, kRowsWide) + a.B : a.B;
-    const int64_t own_keys = own + extra * a.B;
-    const int64_t all = hk * (pre_keys * p.pre_tiles + (many ? own_keys / (a.B ? a.B : 1) * own_tiles : own_keys));
-    int64_t per = cdiv(cdiv(all, slots), 128) * 128;
-    if (per < 256) per = 256;
+    // Own keys of a workgroup.  The lengths are only known on the card, so chunks
+    // are equal, and two a slot rather than one even out requests of different
+    // lengths (17 requests of 4k to 32k keys, 8 heads, E4M3: one 130 us, two 111,
+    // four 129); each request leaves part of a chunk over.  512 keys at least: a
+    // workgroup's start and the join cost as much as some 400 (333 keys in one
+    // workgroup a head 9 us, in two and a join 12.5).
+    auto chunk_of = [&](int64_t extra) {
+        const int64_t own = total + extra * a.B;
+        const int64_t work = hk * (many ? own / a.B * own_tiles : own);
+        int64_t room = slots * 2 - (many ? 0 : hk * a.B / 2);
+        if (room < slots / 2) room = slots / 2;
+        const int64_t per = cdiv(cdiv(work, room), 128) * 128;
+        return per < 512 ? (int64_t)512 : per;
+    };
+    // A request's workgroups walk the prefix themselves if there is nobody to share
+    // it with; if its rows fill 16 tiles, where a product for all gains nothing and
+    // parts to join cost (4 prompts of 1517 tokens behind 4096: 550 us, shared 637;
+    // 8 of 200 behind 2000: 116, shared 101); and if then no join is left and the
+    // reads that could have been shared take less time than it, about 40 MB (64
+    // requests of 300 keys behind 128: 21.5 us, shared 31; behind 1000: 47, 33).
+    if (P > 0)
+        p.joint = a.B == 1 || rows >= a.B * 16 * kRowsWide ||
+                  (P + a.max_kv <= chunk_of(P) && P * (a.B - 1) * hk * a.kv.head_dim * 2 * bytes <= (int64_t)40 << 20);
+    const int64_t extra = p.joint ? P : 0, pre_keys = p.joint ? 0 : P;
+    int64_t pre_units = 0, many_units = 0;
     if (pre_keys) {
-        p.pre_parts = (int)cdiv(pre_keys, per);
+        p.pre_few = rows <= kFewTiles * kCols;
+        p.pre_tiles = (int)cdiv(rows, p.pre_few ? kCols : kRowsWide);
+        // The prefix's workgroups (bound by the matrix units) run beside those of the
+        // own keys (bound by memory), in half the slots: one a CU.  A workgroup for
+        // every slot writes and joins twice the parts (64 requests of 500 keys behind
+        // 16384, 32/8 heads: 53 us, 66 so, 62 with a quarter of the slots).
+        int64_t pp = cdiv(cdiv(hk * pre_keys * p.pre_tiles, slots / 2), 64) * 64;
+        if (pp < 512) pp = 512;
+        p.pre_parts = (int)cdiv(pre_keys, pp);
+        if (p.pre_parts > kMaxParts) p.pre_parts = kMaxParts;
         p.pre_chunk = (int)(cdiv(cdiv(pre_keys, p.pre_parts), 64) * 64);
         p.pre_parts = (int)cdiv(pre_keys, p.pre_chunk);
-        const int64_t groups = hk * p.pre_parts;
-        p.pre_units = (groups % 8 == 0 || groups >= 32 ? cdiv(groups, 8) * 8 : groups) * p.pre_tiles;
+        pre_units = group_units(hk * p.pre_parts, p.pre_tiles);
     }
-    const int64_t longest = a.max_kv + extra;
-    int64_t parts = cdiv(longest, per);
-    if (parts < 1) parts = 1;
-    p.few_parts = (int)parts;
-    p.few_chunk = (int)(cdiv(cdiv(longest > 0 ? longest : 1, parts), 128) * 128);
-    p.few_parts = (int)(longest > 0 ? cdiv(longest, p.few_chunk) : 1);
-    p.few_units = a.B * hk * p.few_parts;
+    const int64_t longest = a.max_kv + extra > 0 ? a.max_kv + extra : 1;
+    int64_t parts = cdiv(longest, chunk_of(extra));
+    if (parts > kMaxParts) parts = kMaxParts;
+    p.few_chunk = (int)(cdiv(cdiv(longest, parts), 128) * 128);
+    p.few_parts = (int)cdiv(longest, p.few_chunk);
+    p.few_tiles = a.max_new * G > kCols ? kFewTiles : 1;
+    const int64_t few_units = a.B * hk * p.few_parts * p.few_tiles;
     if (many) {
         p.many_chunk = p.few_chunk;
         p.many_parts = p.few_parts;
-        p.many_tiles = (int)cdiv(a.max_new * G, kRowsWide);
-        const int64_t groups = a.B * hk * p.many_parts;
-        p.many_units = (groups % 8 == 0 || groups >= 32 ? cdiv(groups, 8) * 8 : groups) * p.many_tiles;
+        p.many_tiles = (int)(rows / kRowsWide + a.B);
+        many_units = group_units(hk * p.many_parts, p.many_tiles);
     }
     p.own_parts = p.few_parts > p.many_parts ? p.few_parts : p.many_parts;
     p.parts = p.pre_parts + p.own_parts;
-    return p;
+    const int64_t units = pre_units + few_units + many_units;
+    if (units >= (int64_t)1 << 24) return -1;
+    p.pre_units = (uint32_t)pre_units;
+    p.few_units = (uint32_t)few_units;
+    p.many_units = (uint32_t)many_units;
+    p.by_heads = FastDiv::of((uint32_t)hk);
+    p.by_few_parts = FastDiv::of((uint32_t)p.few_parts);
+    if (p.pre_tiles) p.by_pre_tiles = FastDiv::of((uint32_t)p.pre_tiles);
+    if (many) p.by_many_tiles = FastDiv::of((uint32_t)p.many_tiles);
+    return units;
 }
 
 static size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
-static int64_t units_of(const Plan& p) { return p.pre_units + p.few_units + p.many_units; }
-
 size_t attn_workspace(const AttnArgs& a) {
-    const Plan p = make_plan(a);
-    if (units_of(p) >= (int64_t)1 << 24) return SIZE_MAX;
+    Plan p;
+    if (make_plan(a, p) < 0) return SIZE_MAX;
     if (p.parts == 1) return 0;
     const size_t rows = (size_t)a.T * a.q_heads;
     return up256((size_t)p.parts * rows * a.kv.head_dim * 4) + 2 * up256((size_t)p.parts * rows * 4) + up256((size_t)a.T * 4);
@@ -922,7 +1051,8 @@ static hipError_t launch_dim(const KArgs& ka, int64_t units) {
 hipError_t attn_launch(const AttnArgs& a) {
     KArgs ka{};
     ka.a = a;
-    ka.p = make_plan(a);
+    const int64_t units = make_plan(a, ka.p);
+    if (units < 1) return hipErrorInvalidConfiguration;
     ka.G = a.q_heads / a.kv.kv_heads;
     ka.per_group = FastDiv::of((uint32_t)ka.G);
     if (ka.p.parts > 1) {
@@ -936,19 +1066,26 @@ hipError_t attn_launch(const AttnArgs& a) {
         w += up256((size_t)ka.p.parts * rows * 4);
         ka.part_n = (int32_t*)w;
     }
-    const int64_t units = units_of(ka.p);
-    if (units < 1 || units >= (int64_t)1 << 24) return hipErrorInvalidConfiguration;
     const int dp = pad_dim(a.kv.head_dim);
     hipError_t e = dp == 64 ? launch_dim<64>(ka, units) : dp == 128 ? launch_dim<128>(ka, units) : launch_dim<256>(ka, units);
     if (e != hipSuccess || ka.p.parts == 1) return e;
-    const int rpw = kThreads / (a.kv.head_dim / 4);
-    const int64_t wgs = cdiv(a.T * a.q_heads, rpw);
+    // As many rows a workgroup as its threads hold; with fewer rows than fill the
+    // card so, fewer rows and the parts side by side.
+    const int fit = kThreads / (a.kv.head_dim / 4);
+    const int64_t rows = a.T * a.q_heads;
+    int rpw = 1;
+    while (rpw * 2 <= fit && rpw < 16 && rows / (rpw * 2) >= 512) rpw *= 2;
+    int spl = fit / rpw;
+    if (spl > ka.p.parts) spl = ka.p.parts;
+    const int64_t wgs = cdiv(rows, rpw);
+    size_t shared = (size_t)rpw * ka.p.parts * 4;
+    if (shared < (size_t)spl * rpw * a.kv.head_dim * 4) shared = (size_t)spl * rpw * a.kv.head_dim * 4;
     if (plan_recorder()) {
         plan_record("attn_join<%s> grid=%lld parts=%d", a.bf16 ? "bf16" : "fp16", (long long)wgs, ka.p.parts);
         return hipSuccess;
     }
-    if (a.bf16) hipLaunchKernelGGL((attn_join_kernel<true>), dim3((unsigned)wgs), dim3(kThreads), 0, a.stream, ka);
-    else hipLaunchKernelGGL((attn_join_kernel<false>), dim3((unsigned)wgs), dim3(kThreads), 0, a.stream, ka);
+    if (a.bf16) hipLaunchKernelGGL((attn_join_kernel<true>), dim3((unsigned)wgs), dim3(kThreads), shared, ka.a.stream, ka, rpw, spl);
+    else hipLaunchKernelGGL((attn_join_kernel<false>), dim3((unsigned)wgs), dim3(kThreads), shared, ka.a.stream, ka, rpw, spl);
     return hipGetLastError();
 }
 

@@ -150,10 +150,22 @@ def _dp(t):
     return t.data_ptr()
 
 
+_raw_stream = None  # gives the handle of torch's current stream
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            # the handle alone: a Stream object made for every call costs 2.5 us more
+            of, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+            if of and dev:
+                torch.cuda.init()
+                _raw_stream = lambda: of(dev())  # noqa: E731
+            else:
+                _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
