@@ -33,25 +33,37 @@ __device__ __forceinline__ int owner_of(const int32_t* first, int n, int32_t i) 
 // It then writes its share of the tokens, the new table entries and the
 // per-request outputs; each token and each new page finds its request by
 // bisection.  A page taken in this very call is looked up in free_blocks, not in
-// the table, so no workgroup waits for another.
-constexpr int kSlotThreads = 256;
+// the table, so no workgroup waits for another.  Nothing but latency bounds it:
+// lengths, sums, bisection, table entry, store (8 requests 2.8 us, 1500 requests
+// with 42 thousand tokens 6.7 us).
+constexpr int kSlotThreads = 512;
+
+// Pages that the first n tokens of a request take.
+__device__ __forceinline__ int32_t pages_of(const FastDiv& per_block, int32_t n) { return n ? (int32_t)per_block.div(n - 1) + 1 : 0; }
 
 __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(KvSlotsArgs a) {
-    __shared__ int32_t s_cu[HQ_KV_MAX_REQUESTS + 1], s_al[HQ_KV_MAX_REQUESTS + 1];
+    // cached tokens; new tokens, then their exclusive sums; the same of new pages
+    __shared__ int32_t s_c[HQ_KV_MAX_REQUESTS], s_cu[HQ_KV_MAX_REQUESTS + 1], s_al[HQ_KV_MAX_REQUESTS + 1];
     __shared__ int32_t s_wave[2][kSlotThreads / 64];
     const int tid = threadIdx.x, B = (int)a.B;
+#pragma unroll 4
+    for (int r = tid; r < B; r += kSlotThreads) {
+        const int32_t c = max(a.cached[r], 0), n = max(a.fresh[r], 0), kv = sat_add(c, n);
+        s_c[r] = c;
+        s_cu[r] = n;
+        s_al[r] = pages_of(a.per_block, kv) - pages_of(a.per_block, c);
+        if (blockIdx.x == 0) a.kv_lens[r] = kv;
+    }
+    __syncthreads();
     const int per = (B + kSlotThreads - 1) / kSlotThreads;  // consecutive requests of a thread
-    const int r0 = tid * per, r1 = r0 + per < B ? r0 + per : B;
+    const int r0 = min(tid * per, B), r1 = min(r0 + per, B);
     int32_t sum_n = 0, sum_p = 0;
     for (int r = r0; r < r1; ++r) {
-        const int32_t c = a.cached[r] > 0 ? a.cached[r] : 0, n = a.fresh[r] > 0 ? a.fresh[r] : 0;
-        const int32_t kv = sat_add(c, n);
-        const int32_t have = c ? (int32_t)a.per_block.div(c - 1) + 1 : 0, want = kv ? (int32_t)a.per_block.div(kv - 1) + 1 : 0;
+        const int32_t n = s_cu[r], p = s_al[r];
         s_cu[r] = sum_n;
         s_al[r] = sum_p;
         sum_n = sat_add(sum_n, n);
-        sum_p = sat_add(sum_p, want - have);
-        if (blockIdx.x == 0) a.kv_lens[r] = kv;
+        sum_p = sat_add(sum_p, p);
     }
     int32_t in_n = sum_n, in_p = sum_p;  // inclusive sums over the wave's threads
     for (int off = 1; off < 64; off <<= 1) {
@@ -98,8 +110,7 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(KvSlotsArgs a) {
     const int64_t start = (int64_t)blockIdx.x * kSlotThreads + tid;
     for (int64_t i = start; i < all_p; i += stride) {
         const int r = owner_of(s_al, B, (int32_t)i);
-        const int32_t c = a.cached[r] > 0 ? a.cached[r] : 0;
-        const int64_t col = (c ? (int64_t)a.per_block.div(c - 1) + 1 : 0) + (i - s_al[r]);
+        const int64_t col = pages_of(a.per_block, s_c[r]) + (i - s_al[r]);
         if (col < a.max_blocks) a.table[(int64_t)r * a.max_blocks + col] = i < a.n_free ? a.free_blocks[i] : -1;
     }
     for (int64_t t = start; t < a.T_cap; t += stride) {
@@ -107,9 +118,8 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(KvSlotsArgs a) {
         int64_t slot = -1;
         if (t < all_n) {
             const int r = owner_of(s_cu, B, (int32_t)t);
-            const int32_t c = a.cached[r] > 0 ? a.cached[r] : 0;
-            const int32_t pos = sat_add(c, (int32_t)t - s_cu[r]);
-            const int64_t col = a.per_block.div(pos), have = c ? (int64_t)a.per_block.div(c - 1) + 1 : 0;
+            const int32_t pos = sat_add(s_c[r], (int32_t)t - s_cu[r]);
+            const int64_t col = a.per_block.div(pos), have = pages_of(a.per_block, s_c[r]);
             int64_t page = -1;
             if (col < a.max_blocks) {
                 if (col < have) {
@@ -139,28 +149,41 @@ hipError_t kv_slots_launch(const KvSlotsArgs& a) {
 // rotary table
 // ---------------------------------------------------------------------------
 
-// One thread per (position, pair).  position * turns is exact to 2^-53 of its
-// value in 64 bits; taking off the nearest whole number of turns there leaves
-// at most half a turn, which fp32 holds to 2^-25 of a turn, whatever the
-// position.  cos and sin of pi * (2 r) are the math library's.
-__global__ __launch_bounds__(256) void rope_table_kernel(RopeTableArgs a) {
-    const int64_t total = a.count * a.half;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / a.half;
-        const int d = (int)(i - row * a.half);
-        const double turn = (double)(a.first + row) * a.turns[d];
-        const float r = (float)(2.0 * (turn - rint(turn)));
-        float sn, cs;
-        sincospif(r, &sn, &cs);
-        a.table[row * 2 * a.half + d] = cs * (float)a.gain;
-        a.table[row * 2 * a.half + a.half + d] = sn * (float)a.gain;
+// A thread writes `run` consecutive positions of one pair: cos and sin of the
+// first in 64 bits (position * turns is exact to 2^-53 of its value; taking off
+// the nearest whole number of turns leaves at most half a turn, whatever the
+// position), then each next one by turning that by the pair's step, four 64-bit
+// operations, whose error after 32 steps is still below 2^-46; rounded once to
+// fp32.  A library cos and sin for each element was bound by arithmetic (131072
+// positions x 128 elements: 22 us); this is bound by the stores (11 to 12.6 us,
+// 5.3 to 6.1 TB/s; a large fill reaches 6.8).
+__global__ __launch_bounds__(256) void rope_table_kernel(RopeTableArgs a, int run) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row0 = i / a.half * run;
+    if (row0 >= a.count) return;
+    const int d = (int)(i - row0 / run * a.half);
+    const double turn = (double)(a.first + row0) * a.turns[d];
+    double c, s, cs, ss;
+    sincospi(2.0 * (turn - rint(turn)), &s, &c);
+    sincospi(2.0 * a.turns[d], &ss, &cs);  // (fewer than half a turn: base > 1)
+    const int64_t end = min(row0 + run, a.count);
+    float* at = a.table + row0 * 2 * a.half + d;
+    for (int64_t row = row0; row < end; ++row, at += 2 * a.half) {
+        at[0] = (float)(c * a.gain);
+        at[a.half] = (float)(s * a.gain);
+        const double c1 = c * cs - s * ss;
+        s = s * cs + c * ss;
+        c = c1;
     }
 }
 
 hipError_t rope_table_launch(const RopeTableArgs& a) {
-    int64_t wgs = cdiv(a.count * a.half, 256);
-    if (wgs > 16384) wgs = 16384;
-    hipLaunchKernelGGL(rope_table_kernel, dim3((unsigned)wgs), dim3(256), 0, a.stream, a);
+    // longer runs share the cost of their start, as long as there are waves to fill the card
+    const int64_t total = a.count * a.half;
+    int run = 32;
+    while (run > 4 && total / run < 256 * 1024) run /= 2;
+    const int64_t wgs = cdiv(cdiv(a.count, run) * a.half, 256);
+    hipLaunchKernelGGL(rope_table_kernel, dim3((unsigned)wgs), dim3(256), 0, a.stream, a, run);
     return hipGetLastError();
 }
 
@@ -205,7 +228,10 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&f)[8], float scale) {
 }
 
 // A unit is 16 elements of one head: eight pairs of the rotated part, or 16
-// elements that pass through; one thread each, all heads of a token side by side.
+// elements that pass through; one thread each, all heads of a token side by side,
+// so that q, k and v are read and written once in whole lines and the table's row
+// comes from cache.  Bound by memory: 16384 tokens of 64 + 2 x 8 heads of 128 into
+// an 8-bit cache 131 us, 4.9 TB/s (a large copy reaches 5.2).
 template <bool BF16, bool FP8>
 __global__ __launch_bounds__(256) void rope_kv_kernel(RopeKvArgs a) {
 #pragma clang fp contract(off)

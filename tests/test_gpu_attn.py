@@ -196,3 +196,69 @@ def test_cache_beyond_32_bit_offsets():
     torch.cuda.synchronize()
     assert np.array_equal(out.double().cpu().numpy().reshape(want.shape), want)
     assert np.array_equal(ls.double().cpu().numpy(), wl)
+
+
+@pytest.mark.parametrize("n", [8, 9, 15, 16, 17])
+@pytest.mark.parametrize("cache", ["fp16", "fp8"])
+def test_drafts(n, cache):
+    """Around one and two tiles of 32 rows of a request (4 rows a token), at its own
+    keys and at a prefix that few rows share."""
+    note(f"attn drafts {n} {cache}")
+    AttnCase([n + 200, n, n + 33], [n, n, 1], 8, 2, 64, "fp16", cache, prefix=130, seed=n).check()
+    AttnCase([n + 700], [n], 8, 2, 128, "fp16", cache, seed=n).check()
+    AttnCase([5, 6], [min(n, 5), 3], 8, 2, 64, "fp16", cache, prefix=700, seed=n).check()
+
+
+def test_many_requests_of_all_kinds():
+    """300 requests with no, one, a few and many new tokens: every token finds its request."""
+    note("attn 300 requests")
+    rng = np.random.default_rng(3)
+    new = [int(x) for x in rng.choice([0, 0, 1, 1, 3, 12, 40], 300)]
+    new[0], new[150], new[299] = 0, 150, 33
+    lens = [n + int(rng.integers(0, 30)) for n in new]
+    AttnCase(lens, new, 4, 1, 16, "bf16", prefix=20, seed=3).check()
+
+
+def test_very_long_context():
+    """More keys than 256 parts of the smallest chunk hold."""
+    note("attn 140000 keys")
+    AttnCase([140000], [1], 2, 1, 16, "bf16", block=64, seed=8).check()
+    AttnCase([3, 1], [1, 1], 1, 1, 16, "fp16", block=64, prefix=150000, seed=8).check()
+
+
+def test_equal_calls_give_equal_bits():
+    note("attn twice")
+    c = AttnCase([40, 3000, 700], [1, 2, 90], 8, 2, 128, "bf16", "fp8", prefix=1500, seed=9)
+    a, la, _ = c.run()
+    for _ in range(3):
+        b, lb, _ = c.run()
+        assert np.array_equal(a, b) and np.array_equal(la, lb)
+
+
+def test_graph_replays():
+    """A captured call reads lengths and tables as they are at each replay."""
+    from bit_quantized_gemm_w4a16_amd import hq
+    from kv_util import i32
+    note("attn graph")
+    c = AttnCase([900, 40, 333], [1, 1, 1], 8, 2, 128, "bf16", prefix=700, seed=12)
+    _, _, args = c.run()
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(g, stream=s):
+            hq.hq_attn(*args)
+    for lens in ([900, 40, 333], [512, 1, 2], [0, 0, 77], [900, 40, 333]):
+        args[12].copy_(i32(lens))
+        args[14].fill_(5)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        got = args[14].clone()
+        args[14].fill_(6)
+        hq.hq_attn(*args)
+        torch.cuda.synchronize()
+        assert torch.equal(got, args[14])
+        c.kv_lens = lens
+        out, lse, parts = c.oracle()
+        tol, _ = c.bounds(out, lse, parts)
+        assert (np.abs(got[:, :8 * 128].double().cpu().numpy().reshape(out.shape) - out) <= tol).all()
