@@ -37,6 +37,7 @@ constexpr int kFewTiles = 2;                    // tiles of kCols rows up to whi
 constexpr int kRowsWide = kWaves * kCols;       // rows of a workgroup whose waves take different rows
 constexpr int kMaxParts = 256;                  // of the prefix, and of a request's own keys (the join keeps their weights in LDS)
 constexpr int kAll = 0x7FFFFFFF;               // lim0: every row sees every key
+constexpr int kRun = 16;                        // keys of a run, see Stream
 constexpr float kNone = -3.0e38f;               // running maximum before any key
 constexpr float kSlack = 8.f;                   // weights stay below 2^kSlack
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -73,23 +74,14 @@ struct KArgs {
 // staging
 // ---------------------------------------------------------------------------
 
-// LDS tiles of the key rows, where loads of all 64 banks at once must not meet:
-// an operand of K is one 16-byte chunk of 16 rows, a transposing load of V takes
-// 4 rows times 64 bytes (8-bit V: 8 rows times 32 bytes).
-//
-// Tiles that go through registers (many rows) have padded rows, K by 16 bytes
-// and V to 64 modulo 256, so that every operand is one address and a constant.
-template <int DP>
-struct Padded {
-    static constexpr int K = DP * 2 + 16, V = DP * 2 + 64;
-};
-// Tiles that are loaded straight into LDS (few rows) are dense, a row of B bytes
-// after the other, and instead the row's 16-byte chunks c change places: c ^
-// turn(r), with the same pairs of chunks staying neighbours.
+// LDS tiles of key rows are loaded straight from memory, a row of B bytes after
+// the other, with the row's 16-byte chunks c at place c ^ turn(r), so that no
+// access meets in a bank: an operand of K is one chunk of 16 rows, a transposing
+// load of V takes 4 rows times 64 bytes (8-bit V: 8 rows times 32 bytes).
 template <int B>
 __device__ __forceinline__ int turn(int r) {  // 16-bit rows
-    if constexpr (B == 128) return (((r >> 1) & 1) << 2) | (((r >> 2) & 1) << 1);
-    else return ((r & 3) << 2) | (((r >> 2) & 1) << 1);
+    if constexpr (B == 128) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    else return ((r & 3) << 2) | ((r >> 2) & 3);
 }
 template <int B>
 __device__ __forceinline__ int turn8(int r) {  // 8-bit rows: rows 0-3 and 8-11 (4-7 and 12-15) are read together
@@ -241,8 +233,8 @@ struct Rows {
         m = kNone;
         l = 0.f;
     }
-    // Waits for the query loads here: were they still open on some way into a
-    // loop, every first use in it would wait for all loads in flight.
+    // Waits for the query loads here, before the first loads to LDS: the compiler
+    // would wait for those too at the first use.
     __device__ __forceinline__ void ready() {
 #pragma unroll
         for (int s = 0; s < KS; ++s) asm volatile("" : "+v"(q[s].u));
@@ -301,25 +293,31 @@ struct Rows {
                 p[k].u[j] = pack2<BF16>(x, y);
             }
     }
+    // S^T = K Q^T of 32 keys: rows are keys, columns are queries.
+    __device__ __forceinline__ void scores(lds_char* lk, v16f& st) {  // lk: the first of the 32 rows
+        constexpr int B = FP8 ? DP : DP * 2;
+        typedef const __attribute__((address_space(3))) v4u lds_v4u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[i] = 0.f;
+#pragma unroll
+        for (int g = 0; g < DP / 32; ++g) {  // 32 elements: two matrix steps
+            Frag8 f0, f1;
+            if constexpr (FP8) {
+                const v4u u = *(lds_v4u*)(lk + col * B + ((2 * g + half) ^ turn8<B>(col)) * 16);
+                f0.u = widen8<BF16>(u[0], u[1]);
+                f1.u = widen8<BF16>(u[2], u[3]);
+            } else {
+                f0.u = *(lds_v4u*)(lk + col * B + ((4 * g + 2 * half) ^ turn<B>(col)) * 16);
+                f1.u = *(lds_v4u*)(lk + col * B + ((4 * g + 2 * half + 1) ^ turn<B>(col)) * 16);
+            }
+            st = mfma32<BF16>(f0, q[2 * g], st);
+            st = mfma32<BF16>(f1, q[2 * g + 1], st);
+        }
+    }
     // O^T += V^T P^T over 32 keys.  A transposing load gives lane (16 dsel + i16,
     // half) element 16 dsel + i16 of four (8-bit: eight) rows, of which each lane
     // names a part: 8 bytes of one row.
-    __device__ __forceinline__ void values_padded(lds_char* lv, const Frag8 (&p)[2]) {  // lv: the first of the 32 rows
-#if defined(__HIP_DEVICE_COMPILE__)
-        const int i16 = lane & 15, dsel = (lane >> 4) & 1;
-        lds_char* v = lv + (4 * half + (i16 >> 2)) * Padded<DP>::V + 32 * dsel + 8 * (i16 & 3);
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int t = 0; t < DT; ++t) {
-                const v2u a = tr16(v + 16 * k * Padded<DP>::V + 64 * t), b = tr16(v + (16 * k + 8) * Padded<DP>::V + 64 * t);
-                Frag8 vf;
-                vf.u = v4u{a[0], a[1], b[0], b[1]};
-                acc[t] = mfma32<BF16>(vf, p[k], acc[t]);
-            }
-#endif
-    }
-    __device__ __forceinline__ void values_dense(lds_char* lv, const Frag8 (&p)[2]) {
+    __device__ __forceinline__ void values(lds_char* lv, const Frag8 (&p)[2]) {  // lv: the first of the 32 rows
 #if defined(__HIP_DEVICE_COMPILE__)
         const int i16 = lane & 15, dsel = (lane >> 4) & 1;
 #pragma unroll
@@ -419,11 +417,153 @@ struct Task {
 };
 
 // ---------------------------------------------------------------------------
-// few rows: a stream of keys per wave
+// keys on their way to LDS
 // ---------------------------------------------------------------------------
 
 // Zeros for what is loaded into LDS in place of keys that do not exist.
 __device__ __attribute__((aligned(16))) const uint32_t g_zeros[4] = {0, 0, 0, 0};
+
+// 16 bytes a lane from memory to LDS: lane l's go to `to` + 16 l.  The load is
+// written out because the compiler, where it sees one, waits for all of them
+// before any LDS read or barrier; its readers wait by wait_loads instead.  It has
+// no register to return to.
+__device__ __forceinline__ void load_to_lds(const char* src, lds_char* to) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane((int)__builtin_bit_cast(uint32_t, to))), "v"(src)
+                 : "memory", "m0");
+#endif
+}
+
+// The same from a wave-uniform address and 32-bit offsets of the lanes.
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t lane_off, lds_char* to) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane((int)__builtin_bit_cast(uint32_t, to))), "v"(lane_off), "s"(base)
+                 : "memory", "m0");
+#endif
+}
+
+// ROWS keys of a wave at a time: place() finds them, fetch() sends their rows to
+// LDS.  Pages are counted on from the prefix's first to the request's last; the
+// ids of 128 in a row lie in registers, so that a wave asks memory for ids (and
+// then waits for all its loads) only once in so many pages.
+//
+// Where pages hold whole runs of 16 keys (the page size and the prefix are
+// multiples of 16) and all keys are there, their addresses are scalar arithmetic
+// and an offset that each lane keeps.  Else each lane finds one key, and the
+// lanes that load its row get the offset by a shuffle; what is no key, or beyond
+// the head, comes from g_zeros.  (Vector instructions are what the tiles of many
+// rows have least room for: with the second way alone, 6069 tokens of prompts
+// behind 4096 took 607 us instead of 517.)
+template <int DP, bool FP8, int ROWS>
+struct Stream {
+    static constexpr int EB = FP8 ? 1 : 2, B = DP * EB;   // bytes of a row
+    static constexpr int LPR = B / 16, RPL = 64 / LPR;    // lanes of a row, rows of a load
+    static constexpr int NL = ROWS / RPL, RUNS = ROWS / kRun;
+    const KvLayout& kv;
+    const Keys& keys;
+    const char *k, *v;
+    int k1, lane, row_bytes, shared_pages, first = -256;
+    uint32_t bstep, sstep;
+    bool runs, whole = false;
+    int32_t id0 = 0, id1 = 0;  // of pages first + lane, first + 64 + lane
+    int64_t off = -1;          // byte offset of this lane's key in the cache, -1 if there is none
+    uint64_t run[RUNS];        // of the runs' first keys
+    uint32_t in_run[NL];       // this lane's place from there, for each load
+
+    __device__ __forceinline__ Stream(const AttnArgs& a, const Keys& ks, int kvh, int end)
+        : kv(a.kv), keys(ks), k((const char*)a.k_cache + (int64_t)kvh * a.kv.head_stride * EB),
+          v((const char*)a.v_cache + (int64_t)kvh * a.kv.head_stride * EB), k1(end), lane(threadIdx.x & 63), row_bytes(a.kv.head_dim * EB),
+          shared_pages(ks.shared ? (int)a.kv.per_block.div(ks.shared - 1) + 1 : 0), bstep((uint32_t)(a.kv.block_stride * EB)),
+          sstep((uint32_t)(a.kv.slot_stride * EB)),
+          runs(a.kv.block_size % kRun == 0 && ks.shared % kRun == 0 && row_bytes == B && a.kv.slot_stride < (1 << 26)) {
+#pragma unroll
+        for (int n = 0; n < NL; ++n) in_run[n] = (uint32_t)(row_of(n) & (kRun - 1)) * sstep + (uint32_t)chunk_of(n) * 16;
+    }
+    __device__ __forceinline__ int row_of(int n) const { return n * RPL + lane / LPR; }
+    __device__ __forceinline__ int chunk_of(int n) const {
+        const int r = row_of(n);
+        return (lane % LPR) ^ (FP8 ? turn8<B>(r) : turn<B>(r));
+    }
+    __device__ __forceinline__ int page_of(int i, uint32_t& at) const {
+        const bool s = i < keys.shared;
+        const uint32_t j = s ? i : i - keys.shared, b = kv.per_block.div(j);
+        at = j - b * (uint32_t)kv.block_size;
+        return (s ? 0 : shared_pages) + (int)b;
+    }
+    __device__ __forceinline__ int32_t id_of(int page) const {
+        return page < shared_pages ? keys.pre[page] : keys.own[page - shared_pages];
+    }
+    __device__ __forceinline__ void reach(int lo, int hi) {  // ids of pages lo .. hi (at most 65) into the registers
+        if (hi - first >= 128) {
+            uint32_t unused;
+            const int last = page_of(k1 - 1, unused);
+            first = lo;
+            id0 = id_of(min(first + lane, last));
+            id1 = id_of(min(first + 64 + lane, last));
+        }
+    }
+    __device__ __forceinline__ void place(int kb) {  // keys kb .. kb + ROWS - 1 (kb uniform); there is at least one key before k1
+        whole = false;
+        if (runs && kb + ROWS <= k1) {
+            uint32_t at[RUNS];
+            int page[RUNS];
+#pragma unroll
+            for (int j = 0; j < RUNS; ++j) page[j] = page_of(kb + j * kRun, at[j]);
+            reach(page[0], page[RUNS - 1]);
+            whole = true;
+#pragma unroll
+            for (int j = 0; j < RUNS; ++j) {
+                const int p = page[j] - first;
+                const uint32_t id = (uint32_t)(p < 64 ? __builtin_amdgcn_readlane(id0, p) : __builtin_amdgcn_readlane(id1, p - 64));
+                run[j] = (uint64_t)id * bstep + (uint64_t)at[j] * sstep;
+                whole = whole && id < (uint32_t)kv.num_blocks;
+            }
+            if (whole) return;
+        }
+        const int i = kb + (lane & (ROWS - 1));
+        uint32_t at;
+        const int page = page_of(min(i, k1 - 1), at);
+        reach(__builtin_amdgcn_readfirstlane(page), __builtin_amdgcn_readlane(page, ROWS - 1));
+        const int32_t a = __shfl(id0, page - first), b = __shfl(id1, page - first);  // (modulo 64)
+        const uint32_t id = (uint32_t)(page - first < 64 ? a : b);
+        off = i < k1 && id < (uint32_t)kv.num_blocks ? (int64_t)((uint64_t)id * bstep + (uint64_t)at * sstep) : (int64_t)-1;
+    }
+    __device__ __forceinline__ void fetch(const char* base, lds_char* to) {
+        if (whole) {
+#pragma unroll
+            for (int n = 0; n < NL; ++n) load_to_lds(base + run[n * RPL / kRun], in_run[n], to + n * 1024);
+        } else {
+            const uint32_t lo = (uint32_t)off, hi = (uint32_t)((uint64_t)off >> 32);
+#pragma unroll
+            for (int n = 0; n < NL; ++n) {
+                const int64_t o = (int64_t)(((uint64_t)(uint32_t)__shfl((int)hi, row_of(n)) << 32) | (uint32_t)__shfl((int)lo, row_of(n)));
+                load_to_lds(o >= 0 && chunk_of(n) * 16 < row_bytes ? base + o + chunk_of(n) * 16 : (const char*)g_zeros, to + n * 1024);
+            }
+        }
+    }
+};
+
+// Takes what is not finite out of `n` kilobytes of a V tile; true if there was any.
+template <bool BF16, bool FP8>
+__device__ __forceinline__ bool clean(lds_char* lv, int n) {
+    bool bad = false;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        auto at = (__attribute__((address_space(3))) v4u*)(lv + i * 1024 + (threadIdx.x & 63) * 16);
+        const v4u u = *at, f = finite_of<BF16, FP8>(u);
+        bad |= differ(f, u);
+        *at = f;
+    }
+    return bad;
+}
+
+// ---------------------------------------------------------------------------
+// few rows: a stream of keys per wave
+// ---------------------------------------------------------------------------
 
 // Groups of 32 keys that a wave has room for.  16-bit rows fill the LDS of two
 // workgroups a CU with one; with half the bytes of an 8-bit cache a second one
@@ -432,101 +572,48 @@ template <bool FP8>
 constexpr int kStages = FP8 ? 2 : 1;
 
 // At most 32 rows.  The cache is read once, so what bounds this is HBM: each
-// wave takes every fourth group of 32 keys by itself, with no barrier, straight
-// from memory into its own LDS tiles.  The tile of K is free once the scores are
-// there and the tile of V after the value product, and each is asked for again
-// at once, so that nearly all the time both are on their way.  A lane looks up
-// the page of one key; the lanes that load that key's row get it by a shuffle.
-// The waves are joined at the end.
+// wave takes every fourth group of 32 keys by itself, with no barrier, into its
+// own LDS tiles.  The tile of K is free once the scores are there and the tile of
+// V after the value product, and each is asked for again at once, so that nearly
+// all the time both are on their way.  64 requests of 4096 keys, 64/8 heads of
+// 128: 5.4 TB/s in 16 bits, 4.6 in 8, where a large copy reaches 5.2.  The waves
+// are joined at the end.
 template <int DP, bool BF16, bool FP8>
 __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_char* sk, lds_char* sv) {
-    constexpr int EB = FP8 ? 1 : 2, B = DP * EB;   // bytes of a row
-    constexpr int LPR = B / 16, RPL = 64 / LPR;    // lanes of a row, rows of a load
-    constexpr int NL = 32 / RPL;
-    constexpr int NS = kStages<FP8>, TILE = 32 * B;
-    const KvLayout& kv = ka.a.kv;
+    typedef Stream<DP, FP8, 32> S;
+    constexpr int NL = S::NL, NS = kStages<FP8>, TILE = 32 * S::B;
+    constexpr int STEP = kWaves * 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Rows<DP, BF16, FP8> x;
     x.init(ka, w.keys, w.kvh, w.tok0, w.nrows, w.row0, w.k1, w.lim0);
+    S in(ka.a, w.keys, w.kvh, w.k1);
     lds_char* const wk = sk + wave * NS * TILE;  // this wave's tiles
     lds_char* const wv = sv + wave * NS * TILE;
-    const char* kb0 = (const char*)ka.a.k_cache + (int64_t)w.kvh * kv.head_stride * EB;
-    const char* vb0 = (const char*)ka.a.v_cache + (int64_t)w.kvh * kv.head_stride * EB;
-    const uint32_t bstep = (uint32_t)(kv.block_stride * EB), sstep = (uint32_t)(kv.slot_stride * EB);
-    const int D = kv.head_dim, row_bytes = D * EB;
-    int32_t pid;
-    uint32_t pat;
-    bool key = false;  // was the row that was looked up a key
-    auto look = [&](int kb) {
-        key = kb + x.col < w.k1;
-        pid = w.keys.page(kv, min(kb + x.col, w.k1 - 1), pat);
-    };
-    // byte offset of this lane's key in the cache, -1 if there is none
-    int64_t off = -1;
-    auto offset = [&]() {
-        const bool ok = key && (uint32_t)pid < (uint32_t)kv.num_blocks;
-        return ok ? (int64_t)((uint64_t)(uint32_t)pid * bstep + (uint64_t)pat * sstep) : (int64_t)-1;
-    };
-    auto fetch = [&](const char* base, lds_char* to) {
-#if defined(__HIP_DEVICE_COMPILE__)
-        const uint32_t lo = (uint32_t)off, hi = (uint32_t)((uint64_t)off >> 32);
-#pragma unroll
-        for (int n = 0; n < NL; ++n) {
-            const int r = n * RPL + x.lane / LPR;
-            const int c = (x.lane % LPR) ^ (FP8 ? turn8<B>(r) : turn<B>(r));
-            const int64_t o = (int64_t)(((uint64_t)(uint32_t)__shfl((int)hi, r) << 32) | (uint32_t)__shfl((int)lo, r));
-            const char* src = o >= 0 && c * 16 < row_bytes ? base + o + c * 16 : (const char*)g_zeros;
-            __builtin_amdgcn_global_load_lds(src, (lds_ptr)(to + n * 1024), 16, 0, 0);
-        }
-#endif
-    };
-    constexpr int STEP = kWaves * 32;
     int kb = w.k0 + wave * 32;
     bool bad = false;
-    if (w.k0 < w.k1) {
-        look(kb);
+    if (kb < w.k1) in.place(kb);
+    x.ready();
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            if (kb + n * STEP < w.k1) {
-                off = offset();
-                fetch(kb0, wk + n * TILE);
-                fetch(vb0, wv + n * TILE);
-            }
-            look(kb + (n + 1) * STEP);
+    for (int n = 0; n < NS; ++n) {
+        if (kb + n * STEP < w.k1) {
+            if (n) in.place(kb + n * STEP);
+            in.fetch(in.k, wk + n * TILE);
+            in.fetch(in.v, wv + n * TILE);
         }
     }
-    x.ready();
     lds_char *lk = wk, *lv = wv;
     for (; kb < w.k1; kb += STEP) {
         const bool next = kb + STEP < w.k1, more = kb + NS * STEP < w.k1;
         // Loads end in order, and K and V of a group are NL each.  After K of this
-        // group came its V, and K and V of the groups that are already asked for
-        // (and page ids, which can only make these waits longer).
+        // group came its V, and K and V of the groups that are already asked for.
         if (NS == 2 && next) wait_loads<3 * NL>();
         else wait_loads<NL>();
         v16f st;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) st[i] = 0.f;
-#pragma unroll
-        for (int g = 0; g < DP / 32; ++g) {  // 32 elements: two matrix steps
-            Frag8 f0, f1;
-            if constexpr (FP8) {
-                const v4u u = *(const __attribute__((address_space(3))) v4u*)(lk + x.col * B + ((2 * g + x.half) ^ turn8<B>(x.col)) * 16);
-                f0.u = widen8<BF16>(u[0], u[1]);
-                f1.u = widen8<BF16>(u[2], u[3]);
-            } else {
-                lds_char* at = lk + x.col * B + ((4 * g + 2 * x.half) ^ turn<B>(x.col)) * 16;
-                f0.u = *(const __attribute__((address_space(3))) v4u*)at;
-                f1.u = *(const __attribute__((address_space(3))) v4u*)(at + 16);
-            }
-            st = mfma32<BF16>(f0, x.q[2 * g], st);
-            st = mfma32<BF16>(f1, x.q[2 * g + 1], st);
-        }
+        x.scores(lk, st);
         if (more) {
-            off = offset();
+            in.place(kb + NS * STEP);
             wait_lds();  // the tile of K has been read
-            fetch(kb0, lk);
-            look(kb + (NS + 1) * STEP);
+            in.fetch(in.k, lk);
         }
         x.prepare(st, kb);
         Frag8 p[2];
@@ -535,19 +622,11 @@ __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_c
         if (more) wait_loads<(2 * NS - 1) * NL>();
         else if (NS == 2 && next) wait_loads<2 * NL>();
         else wait_loads<0>();
-        if (min(kb + 32, w.k1) > x.wseen) {  // some row does not see some of these keys
-#pragma unroll 1
-            for (int n = 0; n < NL; ++n) {
-                auto at = (__attribute__((address_space(3))) v4u*)(lv + n * 1024 + x.lane * 16);
-                const v4u u = *at, f = finite_of<BF16, FP8>(u);
-                bad |= differ(f, u);
-                *at = f;
-            }
-        }
-        x.values_dense(lv, p);
+        if (min(kb + 32, w.k1) > x.wseen) bad |= clean<BF16, FP8>(lv, NL);  // some row does not see some of these keys
+        x.values(lv, p);
         if (more) {
             wait_lds();  // the tile of V has been read
-            fetch(vb0, lv);
+            in.fetch(in.v, lv);
         }
         if constexpr (NS == 2) {
             lk = lk == wk ? wk + TILE : wk;
@@ -573,7 +652,7 @@ __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_c
 #pragma unroll 1
     for (int i = threadIdx.x; i < rows * (DP / 4); i += kThreads) {
         const int r = i / (DP / 4), d = i % (DP / 4) * 4;
-        if (d >= D) continue;
+        if (d >= ka.a.kv.head_dim) continue;
         float m = s_m[0][r], l = 0.f;
 #pragma unroll
         for (int v = 1; v < kWaves; ++v) m = fmaxf(m, s_m[v][r]);
@@ -592,150 +671,84 @@ __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_c
 // many rows: tiles of keys shared by the waves
 // ---------------------------------------------------------------------------
 
-// Each wave has 32 rows of its own; tiles of 64 keys are staged in LDS for all
-// four, in two buffers.  What bounds this is the matrix units and, with as many
-// cycles, the exponentials, so a wave starts the score product of the next 32
-// keys before it turns the last ones into weights.  K and V come through
-// registers and are asked for one whole tile before they are staged.
+// Each wave has 32 rows of its own; tiles of 64 keys are in LDS for all four, in
+// two buffers.  What bounds this is the matrix units and, with as many cycles,
+// the exponentials, so a wave starts the score product of the next 32 keys before
+// it turns the last ones into weights.  A wave fetches 16 rows of each tile; K of
+// the tile after the next goes where this tile's was once all have read it, half
+// a tile before V does, so each has a whole tile's time to arrive.
 template <int DP, bool BF16, bool FP8>
 __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_char* sk, lds_char* sv) {
-    constexpr int KT = 64;
-    constexpr int EPC = FP8 ? 16 : 8, EB = FP8 ? 1 : 2;
-    constexpr int NL = DP / 4 / EPC;  // 16-byte loads of a thread: a quarter of a row
-    constexpr int KP = Padded<DP>::K, VP = Padded<DP>::V;
-    typedef __attribute__((address_space(3))) v4u lds_v4u;
-    const KvLayout& kv = ka.a.kv;
-    const int tid = threadIdx.x, wave = tid >> 6;
-    const int D = kv.head_dim;
+    typedef Stream<DP, FP8, 16> S;
+    constexpr int KT = 64, NL = S::NL, TILE = KT * S::B, HALF = 32 * S::B;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wrow0 = w.row0 + wave * kCols;
-    const bool wlive = __builtin_amdgcn_readfirstlane(wrow0 < w.nrows);
+    const bool wlive = wrow0 < w.nrows;
     Rows<DP, BF16, FP8> x;
     x.init(ka, w.keys, w.kvh, w.tok0, w.nrows, wrow0, w.k1, w.lim0);
     // keys that every row of the workgroup sees
     const int gseen = min(w.k1, w.lim0 == kAll ? w.k1 : max(w.keys.shared, w.lim0 + (int)ka.per_group.div(w.row0)));
-
-    // staging: four threads a row, chunk 4 n + tid % 4 of it
-    const int sr = tid >> 2, sc = tid & 3;
-    const char* kb0 = (const char*)ka.a.k_cache + (int64_t)w.kvh * kv.head_stride * EB;
-    const char* vb0 = (const char*)ka.a.v_cache + (int64_t)w.kvh * kv.head_stride * EB;
-    const uint32_t bstep = (uint32_t)(kv.block_stride * EB), sstep = (uint32_t)(kv.slot_stride * EB);
-    v4u rk[NL], rv[NL];
-    int32_t pid = -1;
-    uint32_t pat = 0;
-    bool key = false;              // was the row that was looked up a key
-    uint64_t off = 0;              // of the row that is being loaded
-    bool ok = false, okn = false;  // is there a key: in the tile that is staged next, in the one that is loaded
-    auto look = [&](int kt) {
-        key = kt + sr < w.k1;
-        pid = w.keys.page(kv, min(kt + sr, w.k1 - 1), pat);
-    };
-    // What is no key of this workgroup, or beyond the head, reads the cache's first
-    // elements instead and is zeroed before use: no load hides behind a branch.
-    auto settle = [&]() {  // the row that was looked up is the next to load
-        okn = key && (uint32_t)pid < (uint32_t)kv.num_blocks;
-        off = (uint64_t)(okn ? (uint32_t)pid : 0u) * bstep + (uint64_t)(okn ? pat : 0u) * sstep;
-    };
-    auto load = [&](const char* base, v4u (&rg)[NL]) {
-#pragma unroll
-        for (int n = 0; n < NL; ++n) rg[n] = ld16(base + off + ((4 * n + sc) * EPC < D ? (4 * n + sc) * 16 : 0));
-    };
-    auto stage = [&](lds_char* to, v4u (&rg)[NL]) {  // to: this thread's place in its row
-        if (D < DP || !__all(ok)) {
-#pragma unroll
-            for (int n = 0; n < NL; ++n) rg[n] &= ok && (4 * n + sc) * EPC < D ? ~0u : 0u;
-        }
-#pragma unroll
-        for (int n = 0; n < NL; ++n) {
-            if constexpr (FP8) {
-                *(lds_v4u*)(to + 128 * n) = widen8<BF16>(rg[n][0], rg[n][1]);
-                *(lds_v4u*)(to + 128 * n + 16) = widen8<BF16>(rg[n][2], rg[n][3]);
-            } else {
-                *(lds_v4u*)(to + 64 * n) = rg[n];
-            }
-        }
-    };
+    S in(ka.a, w.keys, w.kvh, w.k1);
+    lds_char* const wk = sk + wave * 16 * S::B;  // this wave's rows of a tile
+    lds_char* const wv = sv + wave * 16 * S::B;
+    const int mine = wave * 16;
     bool bad = false;
-    auto stage_v = [&](int kt, lds_char* to) {
-        if (min(kt + KT, w.k1) > gseen) {  // some row does not see some of these keys
-#pragma unroll
-            for (int n = 0; n < NL; ++n) {
-                const v4u f = finite_of<BF16, FP8>(rv[n]);
-                bad |= ok && differ(f, rv[n]);
-                rv[n] = f;
-            }
-        }
-        stage(to, rv);
-    };
-    auto scores = [&](lds_char* k, v16f& st) {  // k: this lane's row and half
-#pragma unroll
-        for (int i = 0; i < 16; ++i) st[i] = 0.f;
-#pragma unroll
-        for (int s = 0; s < DP / 16; ++s) {
-            Frag8 kf;
-            kf.u = *(const lds_v4u*)(k + 64 * (s >> 1) + 16 * (s & 1));
-            st = mfma32<BF16>(kf, x.q[s], st);
+    // Where some row does not see some key, V is cleaned by those that fetched it.
+    auto ready_v = [&](int kt, int at) {
+        if (min(kt + KT, w.k1) > gseen) {
+            bad |= clean<BF16, FP8>(wv + at, NL);
+            __syncthreads();
         }
     };
-    lds_char* const put_k = sk + sr * KP + sc * (FP8 ? 32 : 16);
-    lds_char* const put_v = sv + sr * VP + sc * (FP8 ? 32 : 16);
-    lds_char* const get_k = sk + x.col * KP + 32 * x.half;
     v16f s0, s1;
     Frag8 p[2];
-    if (w.k0 < w.k1) {
-        look(w.k0);
-        settle();
-        load(kb0, rk);
-        load(vb0, rv);
-        ok = okn;
-        look(w.k0 + KT);
-    }
+    if (w.k0 < w.k1) in.place(w.k0 + mine);
     x.ready();
     if (w.k0 < w.k1) {
-        stage(put_k, rk);
-        settle();
-        load(kb0, rk);
-        look(w.k0 + 2 * KT);
-        stage_v(w.k0, put_v);
-        load(vb0, rv);
-        ok = okn;
+        in.fetch(in.k, wk);
+        in.fetch(in.v, wv);
+        in.place(w.k0 + KT + mine);
+        in.fetch(in.k, wk + TILE);
+        in.fetch(in.v, wv + TILE);
+        wait_loads<2 * NL>();  // the first tile is there: the second is younger
         __syncthreads();
+        ready_v(w.k0, 0);
         if (wlive) {
-            scores(get_k, s0);
+            x.scores(sk, s0);
             x.prepare(s0, w.k0);
         }
     }
-    // Tile kt from one buffer while tile kt + 64 goes into the other.  On entry:
-    // the scores of its first 32 keys, and the next tile in registers.  The loads
-    // are the same on every way through, at the end of nothing but zeros to be, so
-    // that each is waited for by its place in the queue.
-    auto step = [&](int kt, int kc, int vc, int kn, int vn) {
+    // One tile from the buffers at `at`; the next is at `nx`.  On entry: the scores
+    // of its first 32 keys.  The same loads are asked for on every way through, at the
+    // end for nothing but zeros, so that each is waited for by its place in the queue.
+    auto step = [&](int kt, int at, int nx) {
         const bool more = kt + KT < w.k1;
-        stage(put_k + kn, rk);
-        settle();
-        load(kb0, rk);
-        look(kt + 3 * KT);
         if (wlive) {
-            scores(get_k + kc + 32 * KP, s1);
+            x.scores(sk + at + HALF, s1);
             x.weights(s0, p);
-            x.values_padded(sv + vc, p);
+            x.values(sv + at, p);
             x.prepare(s1, kt + 32);
         }
-        __syncthreads();  // K of the next tile is there
-        stage_v(kt + KT, put_v + vn);
-        load(vb0, rv);
-        ok = okn;
+        wait_loads<NL>();  // K of the next tile: only its V is younger
+        __syncthreads();   // and this tile's K has been read
+        in.place(kt + 2 * KT + mine);
+        in.fetch(in.k, wk + at);
         if (wlive) {
-            if (more) scores(get_k + kn, s0);
+            if (more) x.scores(sk + nx, s0);
             x.weights(s1, p);
-            x.values_padded(sv + vc + 32 * VP, p);
+            x.values(sv + at + HALF, p);
             if (more) x.prepare(s0, kt + KT);
         }
-        __syncthreads();  // V of the next tile is there, and this tile is done with
+        wait_loads<NL>();  // V of the next tile: only the K just asked for is younger
+        __syncthreads();   // and this tile's V has been read
+        in.fetch(in.v, wv + at);
+        if (more) ready_v(kt + KT, nx);
     };
     for (int kt = w.k0; kt < w.k1; kt += 2 * KT) {
-        step(kt, 0, 0, KT * KP, KT * VP);
-        if (kt + KT < w.k1) step(kt + KT, KT * KP, KT * VP, 0, 0);
+        step(kt, 0, TILE);
+        if (kt + KT < w.k1) step(kt + KT, TILE, 0);
     }
+    wait_loads<0>();  // nothing is on its way to LDS any more
     x.l += other_half(x.l);
     if (__syncthreads_or(bad) && wlive) x.add_nonfinite(ka, w.keys, w.kvh, gseen < w.k0 ? w.k0 : w.k0 + (gseen - w.k0) / KT * KT, w.k0, w.k1, 1, 0);
     // each wave's rows through its own share of the tiles' LDS, so that whole rows are written
@@ -752,7 +765,7 @@ __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_
 #pragma unroll 4
     for (int i = x.lane; i < rows * (DP / 4); i += 64) {
         const int r = i / (DP / 4), d = i % (DP / 4) * 4;
-        if (d < D) put<BF16, FP8>(ka, w.kvh, w.tok0, wrow0 + r, d, *(const lds_v4f*)(o + r * R::kPitch + d), s_m[wave][r], s_l[wave][r], w.part, w.direct);
+        if (d < ka.a.kv.head_dim) put<BF16, FP8>(ka, w.kvh, w.tok0, wrow0 + r, d, *(const lds_v4f*)(o + r * R::kPitch + d), s_m[wave][r], s_l[wave][r], w.part, w.direct);
     }
 }
 
@@ -788,8 +801,10 @@ __device__ __forceinline__ int find_request(const int32_t* cu, int B, int tile, 
 
 template <int DP, bool BF16, bool FP8>
 __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(KArgs ka) {
-    // two tiles of 64 padded rows of K and of V, or four waves' 32 dense rows (and then two waves' results in s_k)
-    __shared__ __attribute__((aligned(16))) char s_k[2 * 64 * Padded<DP>::K], s_v[2 * 64 * Padded<DP>::V];
+    // two tiles of 64 rows of K and of V, or the four waves' tiles of 32 (8 bits:
+    // twice two); then the results of two waves in each
+    constexpr int kTiles = 2 * 64 * DP * 2, kResults = 2 * kCols * Rows<DP, BF16, FP8>::kPitch * 4;
+    __shared__ __attribute__((aligned(16))) char s_k[kTiles > kResults ? kTiles : kResults], s_v[kTiles > kResults ? kTiles : kResults];
     const AttnArgs& a = ka.a;
     const Plan& p = ka.p;
     uint32_t id = blockIdx.x;
