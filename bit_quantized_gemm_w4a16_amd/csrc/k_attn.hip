@@ -719,10 +719,10 @@ __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_
         }
     }
     // One tile from the buffers at `at`; the next is at `nx`.  On entry: the scores
-    // of its first 32 keys.  The same loads are asked for on every way through, at the
-    // end for nothing but zeros, so that each is waited for by its place in the queue.
+    // of its first 32 keys.  The last one asks for tiles of nothing but zeros and
+    // scores one: with the same steps on every way through, each load is waited for
+    // by its place in the queue.
     auto step = [&](int kt, int at, int nx) {
-        const bool more = kt + KT < w.k1;
         if (wlive) {
             x.scores(sk + at + HALF, s1);
             x.weights(s0, p);
@@ -734,15 +734,15 @@ __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_
         in.place(kt + 2 * KT + mine);
         in.fetch(in.k, wk + at);
         if (wlive) {
-            if (more) x.scores(sk + nx, s0);
+            x.scores(sk + nx, s0);
             x.weights(s1, p);
             x.values(sv + at + HALF, p);
-            if (more) x.prepare(s0, kt + KT);
+            x.prepare(s0, kt + KT);
         }
         wait_loads<NL>();  // V of the next tile: only the K just asked for is younger
         __syncthreads();   // and this tile's V has been read
         in.fetch(in.v, wv + at);
-        if (more) ready_v(kt + KT, nx);
+        if (kt + KT < w.k1) ready_v(kt + KT, nx);
     };
     for (int kt = w.k0; kt < w.k1; kt += 2 * KT) {
         step(kt, 0, TILE);
