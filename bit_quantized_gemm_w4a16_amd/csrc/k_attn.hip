@@ -36,7 +36,7 @@ constexpr int kCols = 32;                       // query rows of a wave's matrix
 constexpr int kFewTiles = 2;                    // tiles of kCols rows up to which a request counts as few rows
 constexpr int kRowsWide = kWaves * kCols;       // rows of a workgroup whose waves take different rows
 constexpr int kMaxParts = 256;                  // of the prefix, and of a request's own keys (the join keeps their weights in LDS)
-constexpr int kAll = 0x7FFFFFFF;               // lim0: every row sees every key
+constexpr int kAll = 0x7FFFFFFF;                // lim0: every row sees every key
 constexpr int kRun = 16;                        // keys of a run, see Stream
 constexpr float kNone = -3.0e38f;               // running maximum before any key
 constexpr float kSlack = 8.f;                   // weights stay below 2^kSlack
@@ -46,7 +46,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // prefix (all rows of a key head, the shared keys), few (a request with at most
 // kCols rows per key head: the four waves take different keys of each tile and
 // are joined at the end; up to kFewTiles such tiles of one request) and many (a
-// request with more rows: the waves take different rows).  `joint`: a request's workgroups walk the prefix themselves.
+// request with more rows: the waves take different rows).  `joint`: a request's
+// workgroups walk the prefix themselves.
 struct Plan {
     int pre_tiles, pre_parts, pre_chunk;
     bool pre_few;                    // the rows at the prefix count as few
@@ -279,7 +280,7 @@ struct Rows {
         }
     }
     // Weights of the 32 keys, rounded to 16 bits as the operands of the value
-    // product (relative error 2^-9 or 2^-12 each, like the output's own rounding);
+    // product (relative error up to 2^-8 or 2^-11 each, like the output's own);
     // their sum is of the unrounded ones.
     __device__ __forceinline__ void weights(const v16f& st, Frag8 (&p)[2]) {
 #pragma unroll
@@ -855,26 +856,26 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(KArgs
         int64_t t0 = a.cu[r], t1 = a.cu[r + 1];
         t0 = t0 < 0 ? 0 : t0;
         t1 = t1 > a.T ? a.T : t1;
-        const int n = t1 > t0 ? (int)min(t1 - t0, a.max_new) : 0;
+        const int fresh = t1 > t0 ? (int)(t1 - t0) : 0;
         tok0 = t0;
-        rows = n * ka.G;
+        rows = (int)min((int64_t)fresh, a.max_new) * ka.G;
         row0 = tile * (few ? kCols : kRowsWide);
         if (few != (rows <= kFewTiles * kCols) || row0 >= rows) return;
-        int64_t len = a.kv_lens[r];
-        len = len < 0 ? 0 : min(min(len, a.max_kv), a.max_blocks * a.kv.block_size);
+        const int64_t len = min(max((int64_t)a.kv_lens[r], (int64_t)0), (int64_t)1 << 29);
         keys.own = a.block_table + (int64_t)r * a.max_blocks;
         keys.shared = p.joint ? (int)a.prefix_len : 0;
-        lim0 = keys.shared + (int)len - n + 1;
+        lim0 = keys.shared + (int)len - fresh + 1;
+        const int held = keys.shared + (int)min(min(len, a.max_kv), a.max_blocks * a.kv.block_size);  // keys that can be read
         const int chunk = few ? p.few_chunk : p.many_chunk;
         const int last = min(row0 + (few ? kCols : kRowsWide), rows) - 1;
-        const int end = max(keys.shared, lim0 + (int)ka.per_group.div(last));  // keys that the tile's last row sees
+        const int end = min(held, max(keys.shared, lim0 + (int)ka.per_group.div(last)));  // keys that the tile's last row sees
         k0 = (int64_t)part * chunk;
         base = p.pre_parts;
         // how many parts each token's own keys have, for the join
         if (!direct && part == 0 && kvh == 0)
             for (int i = threadIdx.x; i <= last - row0; i += kThreads) {
                 const int t = (int)ka.per_group.div(row0 + i);
-                ka.part_n[t0 + t] = (max(keys.shared, lim0 + t) + chunk - 1) / chunk;
+                ka.part_n[t0 + t] = (min(held, max(keys.shared, lim0 + t)) + chunk - 1) / chunk;
             }
         if (k0 >= end && !(direct && part == 0)) return;
         k1 = (int)min(k0 + chunk, (int64_t)end);
@@ -1024,7 +1025,8 @@ static int64_t make_plan(const AttnArgs& a, Plan& p) {
     p.own_parts = p.few_parts > p.many_parts ? p.few_parts : p.many_parts;
     p.parts = p.pre_parts + p.own_parts;
     const int64_t units = pre_units + few_units + many_units;
-    if (units >= (int64_t)1 << 24) return -1;
+    // fewer than 2^32 threads in a launch; the join has 4 rows a workgroup or more when there are many
+    if (units >= (int64_t)1 << 24 || (p.parts > 1 && cdiv(a.T * a.q_heads, 4) >= (int64_t)1 << 24)) return -1;
     p.pre_units = (uint32_t)pre_units;
     p.few_units = (uint32_t)few_units;
     p.many_units = (uint32_t)many_units;

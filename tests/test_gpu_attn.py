@@ -262,3 +262,22 @@ def test_graph_replays():
         out, lse, parts = c.oracle()
         tol, _ = c.bounds(out, lse, parts)
         assert (np.abs(got[:, :8 * 128].double().cpu().numpy().reshape(out.shape) - out) <= tol).all()
+
+
+@pytest.mark.parametrize("prefix", [0, 900])
+def test_bounds_smaller_than_the_lengths(prefix):
+    """A max_new or max_kv that is too small leaves tokens or keys out; the rest is as it should be."""
+    note(f"attn tight bounds prefix {prefix}")
+    c = AttnCase([40, 700, 90], [1, 50, 20], 8, 2, 64, "bf16", prefix=prefix, seed=9)
+    out, lse, parts = c.oracle()
+    tol, _ = c.bounds(out, lse, parts)
+    got, _, _ = c.run(max_new=30)
+    rows = np.r_[0:31, 51:71]  # the first 30 tokens of the second request, all others
+    assert (np.abs(got - out) <= tol)[rows].all()
+    got, _, _ = c.run(max_kv=64)   # a request's keys from 64 on do not count
+    assert (np.abs(got - out) <= tol)[0].all()
+    k, v = c.held(0, 1)[:prefix + 64], c.held(1, 1)[:prefix + 64]
+    from oracle import kv as okv
+    o2, l2, p2 = okv.attention(c.q[1:51].double().numpy(), lambda r: k, lambda r: v, prefix, [64 + 49], [0, 50], float(np.float32(c.scale)))
+    t2, _ = c.bounds(o2, l2, p2)
+    assert (np.abs(got[1:51] - o2) <= t2).all()
