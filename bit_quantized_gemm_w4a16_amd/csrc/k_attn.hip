@@ -972,28 +972,66 @@ static int64_t make_plan(const AttnArgs& a, Plan& p) {
     // Own keys of a workgroup.  The lengths are only known on the card, so chunks
     // are equal, and two a slot rather than one even out requests of different
     // lengths (17 requests of 4k to 32k keys, 8 heads, E4M3: one 130 us, two 111,
-    // four 129); each request leaves part of a chunk over.  512 keys at least: a
-    // workgroup's start and the join cost as much as some 400 (333 keys in one
-    // workgroup a head 9 us, in two and a join 12.5).
+    // four 129).  Where that gives 512 keys or fewer, a workgroup's time is latency.
+    // If those of 256 keys take half the slots at most: one part up to 640 keys, for
+    // a join costs as much as some 400 (8 requests of 600 keys, 32/8 heads: one part
+    // 11.5 us, two 13.4, three 12.6), else 256 a workgroup (900 keys: 13.3 us, with
+    // 512 a workgroup 15.3; 700 keys of 256, 16/1 heads: 17.6, in two parts 19.6, in
+    // one 20.7).  With more workgroups, one part up to 768 (64 requests of 700 keys:
+    // 31 us, in two 38), else 512 (8 of 4000: 28.6, with 256 32).
     auto chunk_of = [&](int64_t extra) {
-        const int64_t own = total + extra * a.B;
+        const int64_t own = total + extra * a.B, longest = a.max_kv + extra;
         const int64_t work = hk * (many ? own / a.B * own_tiles : own);
         int64_t room = slots * 2 - (many ? 0 : hk * a.B / 2);
         if (room < slots / 2) room = slots / 2;
         const int64_t per = cdiv(cdiv(work, room), 128) * 128;
-        return per < 512 ? (int64_t)512 : per;
+        if (per > 512) return per;
+        const bool small = work <= slots / 2 * 256;
+        if (longest <= (small ? 640 : 768)) return (int64_t)768;
+        return small && !many && P == extra ? (int64_t)256 : (int64_t)512;
     };
     // A request's workgroups walk the prefix themselves if there is nobody to share
     // it with; if its rows fill 16 tiles, where a product for all gains nothing and
     // parts to join cost (4 prompts of 1517 tokens behind 4096: 550 us, shared 637;
-    // 8 of 200 behind 2000: 116, shared 101); and if then no join is left and the
-    // reads that could have been shared take less time than it, about 40 MB (64
-    // requests of 300 keys behind 128: 21.5 us, shared 31; behind 1000: 47, 33).
+    // 8 of 200 behind 2000: 116, shared 101); and if then no join is left and what
+    // could have been shared takes less time than it, about 128 MB out of the L2s
+    // (32/8 heads, 64 requests of 100 keys behind 400, 103 MB: 13.8 us, shared 20.6;
+    // 256 of 200 behind 128, 134 MB: 45.7, 48.4; behind 256, 267 MB: 50.6, 48.6).
     if (P > 0)
         p.joint = a.B == 1 || rows >= a.B * 16 * kRowsWide ||
-                  (P + a.max_kv <= chunk_of(P) && P * (a.B - 1) * hk * a.kv.head_dim * 2 * bytes <= (int64_t)40 << 20);
+                  (P + a.max_kv <= chunk_of(P) && P * (a.B - 1) * hk * a.kv.head_dim * 2 * bytes <= (int64_t)128 << 20);
     const int64_t extra = p.joint ? P : 0, pre_keys = p.joint ? 0 : P;
+    const int64_t longest = a.max_kv + extra > 0 ? a.max_kv + extra : 1, per = chunk_of(extra);
+    auto split = [&](int64_t keys, int64_t per, int64_t step, int& chunk, int& parts) {  // equal chunks of about `per` keys
+        int64_t n = cdiv(keys, per);
+        if (n > kMaxParts) n = kMaxParts;
+        chunk = (int)(cdiv(cdiv(keys, n), step) * step);
+        parts = (int)cdiv(keys, chunk);
+    };
+    // If there is a join all the same, and a part of all rows is little to write and
+    // read (8 MB are some 1.6 us), workgroups with a tile of rows to go through take
+    // fewer than 512 keys while there are slots for them (below; 3 requests of 100
+    // tokens behind 900 keys and 300, 40 heads, 12 MB a part: 42 us, with short
+    // chunks 47).
+    const bool cheap = a.T * a.q_heads * a.kv.head_dim * 8 <= (int64_t)8 << 20;
+    split(longest, per, 128, p.few_chunk, p.few_parts);
+    p.few_tiles = a.max_new * G > kCols ? kFewTiles : 1;
+    const int64_t few_units = a.B * hk * p.few_parts * p.few_tiles;
     int64_t pre_units = 0, many_units = 0;
+    if (many) {
+        // Tiles of 128 rows take 64 keys in 2 to 4 us: as many parts as fill the slots
+        // once with half of the last tiles there, 256 keys at least (16 requests of 12
+        // tokens at 3000 keys, 16/2 heads: 34 us in 6 parts, 31.5 in 12).
+        int64_t least = per;
+        if (cheap && (pre_keys || p.few_parts > 1)) {
+            const int64_t n = slots / (hk * (rows / kRowsWide + cdiv(a.B, 2)));
+            least = cdiv(total / a.B + extra, n > 1 ? n : 1);
+            if (least < 256) least = 256;
+        }
+        split(longest, least < per ? least : per, 64, p.many_chunk, p.many_parts);
+        p.many_tiles = (int)(rows / kRowsWide + a.B);
+        many_units = group_units(hk * p.many_parts, p.many_tiles);
+    }
     if (pre_keys) {
         p.pre_few = rows <= kFewTiles * kCols;
         p.pre_tiles = (int)cdiv(rows, p.pre_few ? kCols : kRowsWide);
@@ -1001,26 +1039,23 @@ static int64_t make_plan(const AttnArgs& a, Plan& p) {
         // own keys (bound by memory), in half the slots: one a CU.  A workgroup for
         // every slot writes and joins twice the parts (64 requests of 500 keys behind
         // 16384, 32/8 heads: 53 us, 66 so, 62 with a quarter of the slots).
-        int64_t pp = cdiv(cdiv(hk * pre_keys * p.pre_tiles, slots / 2), 64) * 64;
-        if (pp < 512) pp = 512;
-        p.pre_parts = (int)cdiv(pre_keys, pp);
-        if (p.pre_parts > kMaxParts) p.pre_parts = kMaxParts;
-        p.pre_chunk = (int)(cdiv(cdiv(pre_keys, p.pre_parts), 64) * 64);
-        p.pre_parts = (int)cdiv(pre_keys, p.pre_chunk);
+        const int64_t work = hk * pre_keys * p.pre_tiles, own_units = few_units + many_units;
+        int64_t pp = cdiv(work, slots / 2);
+        if (pp < 512) {
+            // Fewer than 512 keys in the slots that the own keys leave, a quarter at
+            // least, where those do not take longer anyhow (24 requests of 300 keys
+            // behind 1000, 32/8 heads: 31 us in 2 parts, 21 in 8; 64 behind 2000: 33 in
+            // 4, 31 in 8, 34 in 16; 17 of 4k to 32k behind 2011, E4M3: 107 in 4, 111 in
+            // 8).  With few rows 128 keys are one turn: 384 at least (8 requests of 300
+            // behind 2000: 15.7 us with 512, 14.5 with 384, 15.5 with 128).
+            int64_t room = slots - own_units, least = p.pre_few ? 384 : 128;
+            room = room > slots / 2 ? slots / 2 : room < slots / 4 ? slots / 4 : room;
+            if (!cheap || own_units > 2 * slots) least = 512;
+            pp = cdiv(work, room);
+            pp = pp < least ? least : pp > 512 ? 512 : pp;
+        }
+        split(pre_keys, cdiv(pp, 64) * 64, 64, p.pre_chunk, p.pre_parts);
         pre_units = group_units(hk * p.pre_parts, p.pre_tiles);
-    }
-    const int64_t longest = a.max_kv + extra > 0 ? a.max_kv + extra : 1;
-    int64_t parts = cdiv(longest, chunk_of(extra));
-    if (parts > kMaxParts) parts = kMaxParts;
-    p.few_chunk = (int)(cdiv(cdiv(longest, parts), 128) * 128);
-    p.few_parts = (int)cdiv(longest, p.few_chunk);
-    p.few_tiles = a.max_new * G > kCols ? kFewTiles : 1;
-    const int64_t few_units = a.B * hk * p.few_parts * p.few_tiles;
-    if (many) {
-        p.many_chunk = p.few_chunk;
-        p.many_parts = p.few_parts;
-        p.many_tiles = (int)(rows / kRowsWide + a.B);
-        many_units = group_units(hk * p.many_parts, p.many_tiles);
     }
     p.own_parts = p.few_parts > p.many_parts ? p.few_parts : p.many_parts;
     p.parts = p.pre_parts + p.own_parts;
