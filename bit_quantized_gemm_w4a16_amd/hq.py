@@ -143,11 +143,11 @@ def _dp(t):
     """Device (or host numpy) pointer of a tensor/array; None -> NULL."""
     if t is None:
         return None
-    if isinstance(t, np.ndarray):
-        return t.ctypes.data
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    try:
+        ptr = t.data_ptr  # first: a call with 13 tensors takes 1 us less than with two isinstance before it
+    except AttributeError:
+        return t if isinstance(t, int) else t.ctypes.data
+    return ptr()
 
 
 _raw_stream = None  # gives the handle of torch's current stream
