@@ -1008,30 +1008,32 @@ static int64_t make_plan(const AttnArgs& a, Plan& p) {
         chunk = (int)(cdiv(cdiv(keys, n), step) * step);
         parts = (int)cdiv(keys, chunk);
     };
-    // If there is a join all the same, and a part of all rows is little to write and
-    // read (8 MB are some 1.6 us), workgroups with a tile of rows to go through take
-    // fewer than 512 keys while there are slots for them (below; 3 requests of 100
-    // tokens behind 900 keys and 300, 40 heads, 12 MB a part: 42 us, with short
-    // chunks 47).
-    const bool cheap = a.T * a.q_heads * a.kv.head_dim * 8 <= (int64_t)8 << 20;
-    split(longest, per, 128, p.few_chunk, p.few_parts);
-    p.few_tiles = a.max_new * G > kCols ? kFewTiles : 1;
-    const int64_t few_units = a.B * hk * p.few_parts * p.few_tiles;
     int64_t pre_units = 0, many_units = 0;
+    bool whole = false;
     if (many) {
-        // Tiles of 128 rows take 64 keys in 2 to 4 us: as many parts as fill the slots
-        // once with half of the last tiles there, 256 keys at least (16 requests of 12
-        // tokens at 3000 keys, 16/2 heads: 34 us in 6 parts, 31.5 in 12).
-        int64_t least = per;
-        if (cheap && (pre_keys || p.few_parts > 1)) {
-            const int64_t n = slots / (hk * (rows / kRowsWide + cdiv(a.B, 2)));
-            least = cdiv(total / a.B + extra, n > 1 ? n : 1);
-            if (least < 256) least = 256;
+        // Tiles of 128 rows take 64 keys in 2 us or more, so n parts take 35 ns for
+        // each of the longest request's keys / n, or for the slots' share of all keys
+        // if that is more; a part of all rows is written and read at some 2.5 TB/s,
+        // and a join takes 8 us where there would be none (2 requests of 256 tokens at
+        // 6000 keys, 32/8 heads: 78 us in 4 parts, 91 in 7; 3 prompts of some 440 up to
+        // 1048 keys, 40/8, E4M3: 55 in one, 73 in 3; 4 of 64 at 700: 29 in one, 32 in 4).
+        int64_t best = 0, n = 1;
+        const int64_t key = pad_dim(a.kv.head_dim) == 256 ? 70 : 35, avg = total / a.B + extra;
+        const int64_t share = hk * avg * (rows / kRowsWide + cdiv(a.B, 2)) / slots;
+        const int64_t part = a.T * a.q_heads * a.kv.head_dim * 8 / 2500 * avg / longest;  // of the requests that have it
+        for (int64_t i = 1; i <= 64 && i <= cdiv(longest, 128); ++i) {
+            const int64_t keys = cdiv(longest, i), join = i > 1 && !pre_keys ? 8000 : 0;
+            const int64_t ns = key * (keys > share ? keys : share) + (i > 1 || pre_keys ? i * part : 0) + join;
+            if (i == 1 || ns < best) best = ns, n = i;
         }
-        split(longest, least < per ? least : per, 64, p.many_chunk, p.many_parts);
+        split(longest, cdiv(longest, n), 64, p.many_chunk, p.many_parts);
+        whole = n == 1 && !pre_keys;  // the others' rows take less time for as many keys
         p.many_tiles = (int)(rows / kRowsWide + a.B);
         many_units = group_units(hk * p.many_parts, p.many_tiles);
     }
+    split(longest, whole ? longest : per, 128, p.few_chunk, p.few_parts);
+    p.few_tiles = a.max_new * G > kCols ? kFewTiles : 1;
+    const int64_t few_units = a.B * hk * p.few_parts * p.few_tiles;
     if (pre_keys) {
         p.pre_few = rows <= kFewTiles * kCols;
         p.pre_tiles = (int)cdiv(rows, p.pre_few ? kCols : kRowsWide);
@@ -1039,18 +1041,22 @@ static int64_t make_plan(const AttnArgs& a, Plan& p) {
         // own keys (bound by memory), in half the slots: one a CU.  A workgroup for
         // every slot writes and joins twice the parts (64 requests of 500 keys behind
         // 16384, 32/8 heads: 53 us, 66 so, 62 with a quarter of the slots).
-        const int64_t work = hk * pre_keys * p.pre_tiles, own_units = few_units + many_units;
+        const int64_t work = hk * pre_keys * p.pre_tiles;
+        int64_t own_units = total / p.few_chunk + a.B < a.B * p.few_parts ? total / p.few_chunk + a.B : a.B * p.few_parts;
+        if (many) own_units = (rows / kRowsWide + cdiv(a.B, 2)) * cdiv(total / a.B + 1, p.many_chunk);
+        own_units *= hk;
         int64_t pp = cdiv(work, slots / 2);
         if (pp < 512) {
             // Fewer than 512 keys in the slots that the own keys leave, a quarter at
-            // least, where those do not take longer anyhow (24 requests of 300 keys
-            // behind 1000, 32/8 heads: 31 us in 2 parts, 21 in 8; 64 behind 2000: 33 in
-            // 4, 31 in 8, 34 in 16; 17 of 4k to 32k behind 2011, E4M3: 107 in 4, 111 in
-            // 8).  With few rows 128 keys are one turn: 384 at least (8 requests of 300
-            // behind 2000: 15.7 us with 512, 14.5 with 384, 15.5 with 128).
+            // least, where those do not take longer anyhow and a part of all rows is
+            // little to write and read (24 requests of 300 keys behind 1000, 32/8 heads:
+            // 31 us in 2 parts, 21 in 8; 64 behind 2000: 33 in 4, 31 in 8, 34 in 16; 17
+            // of 4k to 32k behind 2011, E4M3: 107 in 4, 111 in 8).  With few rows 128
+            // keys are one turn: 384 at least (8 requests of 300 behind 2000: 15.7 us
+            // with 512, 14.5 with 384, 15.5 with 128).
             int64_t room = slots - own_units, least = p.pre_few ? 384 : 128;
             room = room > slots / 2 ? slots / 2 : room < slots / 4 ? slots / 4 : room;
-            if (!cheap || own_units > 2 * slots) least = 512;
+            if (own_units > slots * 2 || a.T * a.q_heads * a.kv.head_dim * 8 > (int64_t)8 << 20) least = 512;
             pp = cdiv(work, room);
             pp = pp < least ? least : pp > 512 ? 512 : pp;
         }

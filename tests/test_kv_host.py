@@ -125,7 +125,9 @@ def test_attn_size_refusals():
     assert status_of(ws, ATT(q_heads=64, max_new=1 << 20), KV(), 4096, 1 << 20, 300) == hq.HQ_OK   # as many rows, but none to join
     many = dict(q_heads=64, max_new=1 << 20, max_kv=1000, total_kv=1)
     assert status_of(ws, ATT(**many), KV(), 1, (1 << 20) - 1, 0) == hq.HQ_OK
-    assert status_of(ws, ATT(**many), KV(), 1, 1 << 20, 0) == hq.HQ_ERR_UNSUPPORTED   # too many rows to join
+    assert status_of(ws, ATT(**many), KV(), 1, 1 << 20, 0) == hq.HQ_OK   # one part of the keys: none to join
+    assert status_of(ws, ATT(q_heads=64), KV(), 1 << 20, (1 << 20) - 1, 3000) == hq.HQ_OK
+    assert status_of(ws, ATT(q_heads=64), KV(), 1 << 20, 1 << 20, 3000) == hq.HQ_ERR_UNSUPPORTED   # too many rows to join
 
 
 ATTN = dict(desc=None, kv=None, B=2, T=2, q=A, q_stride=512, k_cache=A, v_cache=A, prefix_table=A, prefix_len=600, block_table=A, max_blocks=8,
