@@ -54,8 +54,9 @@ struct Plan {
     int few_parts, few_chunk, few_tiles;
     int many_tiles, many_parts, many_chunk;
     bool joint;
+    bool listed;                     // few's units are those that there are, see find_few
     uint32_t pre_units, few_units, many_units;  // (make_plan checks their sum before it narrows them)
-    FastDiv by_heads, by_pre_tiles, by_few_parts, by_many_tiles;
+    FastDiv by_heads, by_pre_tiles, by_few_parts, by_few_chunk, by_many_tiles;
     int own_parts;                   // partial results of a row from its own keys, at most
     int parts;                       // all partial results of a row; 1: written directly
 };
@@ -800,6 +801,44 @@ __device__ __forceinline__ int find_request(const int32_t* cu, int B, int tile, 
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// The `unit`-th of the parts (and tiles) that the requests with few rows have,
+// from their lengths: a lane counts one request's, and a running sum says whose
+// it is.  False if there are fewer.
+__device__ __forceinline__ bool find_few(const KArgs& ka, int unit, int& r, int& part, int& tile) {
+    const AttnArgs& a = ka.a;
+    const int lane = threadIdx.x & 63, B = (int)a.B, shared = ka.p.joint ? (int)a.prefix_len : 0;
+    for (int b0 = 0; b0 < B; b0 += 64) {
+        int units = 0, tiles = 1;
+        if (b0 + lane < B) {
+            const int i = b0 + lane, t0 = max(a.cu[i], 0), fresh = (int)min((int64_t)a.cu[i + 1], a.T) - t0;
+            const int64_t rows = min((int64_t)max(fresh, 0), a.max_new) * ka.G;
+            if (rows > 0 && rows <= kFewTiles * kCols) {
+                const int64_t len = min(max((int64_t)a.kv_lens[i], (int64_t)0), (int64_t)1 << 29);
+                const int held = shared + (int)min(min(len, a.max_kv), a.max_blocks * a.kv.block_size);
+                const int end = min(held, max(shared, shared + (int)len - fresh + 1 + (int)ka.per_group.div((int)rows - 1)));
+                tiles = rows > kCols ? kFewTiles : 1;
+                units = max((int)ka.p.by_few_chunk.div(end + ka.p.few_chunk - 1), 1) * tiles;
+            }
+        }
+        int sum = units;
+        for (int o = 1; o < 64; o *= 2) {
+            const int v = __shfl_up(sum, o);
+            if (lane >= o) sum += v;
+        }
+        const uint64_t hit = __ballot(sum > unit);
+        if (hit) {
+            const int l = __builtin_ctzll(hit), n = __builtin_amdgcn_readlane(tiles, l);
+            const int at = unit - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(units, l));
+            r = b0 + l;
+            part = n > 1 ? at / kFewTiles : at;
+            tile = at - part * n;
+            return true;
+        }
+        unit -= __builtin_amdgcn_readlane(sum, 63);
+    }
+    return false;
+}
+
 template <int DP, bool BF16, bool FP8>
 __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(KArgs ka) {
     // two tiles of 64 rows of K and of V, or the four waves' tiles of 32 (8 bits:
@@ -836,12 +875,16 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(KArgs
         if (few) {  // heads side by side: together they read whole pages
             uint32_t g = p.by_heads.div(id);
             kvh = (int)(id - g * heads);
-            if (p.few_tiles > 1) {
-                tile = g % kFewTiles;
-                g /= kFewTiles;
+            if (p.listed) {
+                if (!find_few(ka, (int)g, r, part, tile)) return;
+            } else {
+                if (p.few_tiles > 1) {
+                    tile = g % kFewTiles;
+                    g /= kFewTiles;
+                }
+                r = (int)p.by_few_parts.div(g);
+                part = (int)(g - r * p.few_parts);
             }
-            r = (int)p.by_few_parts.div(g);
-            part = (int)(g - r * p.few_parts);
         } else {
             uint32_t group;
             if (!grouped_unit(id - p.few_units, heads * p.many_parts, p.by_many_tiles, group, tile)) return;
@@ -1033,7 +1076,16 @@ static int64_t make_plan(const AttnArgs& a, Plan& p) {
     }
     split(longest, whole ? longest : per, 128, p.few_chunk, p.few_parts);
     p.few_tiles = a.max_new * G > kCols ? kFewTiles : 1;
-    const int64_t few_units = a.B * hk * p.few_parts * p.few_tiles;
+    // Most of requests x parts may be none: workgroups that find no work end at some
+    // 350 a us, so with a quarter of them or more the units are listed from the
+    // lengths (one request for a lane; the sum of the lengths bounds their number; 17
+    // requests of 4k to 32k keys, E4M3: 107 us without the list, 101 with; 73 of up to
+    // 5843, half of them without a new token: 30, 25).
+    int64_t few_units = a.B * p.few_parts;
+    const int64_t there = (total + extra * a.B) / p.few_chunk + a.B;
+    p.listed = a.B <= 512 && there * 4 <= few_units * 3;
+    if (p.listed) few_units = there;
+    few_units *= hk * p.few_tiles;
     if (pre_keys) {
         p.pre_few = rows <= kFewTiles * kCols;
         p.pre_tiles = (int)cdiv(rows, p.pre_few ? kCols : kRowsWide);
@@ -1042,7 +1094,7 @@ static int64_t make_plan(const AttnArgs& a, Plan& p) {
         // every slot writes and joins twice the parts (64 requests of 500 keys behind
         // 16384, 32/8 heads: 53 us, 66 so, 62 with a quarter of the slots).
         const int64_t work = hk * pre_keys * p.pre_tiles;
-        int64_t own_units = total / p.few_chunk + a.B < a.B * p.few_parts ? total / p.few_chunk + a.B : a.B * p.few_parts;
+        int64_t own_units = there < a.B * p.few_parts ? there : a.B * p.few_parts;
         if (many) own_units = (rows / kRowsWide + cdiv(a.B, 2)) * cdiv(total / a.B + 1, p.many_chunk);
         own_units *= hk;
         int64_t pp = cdiv(work, slots / 2);
@@ -1072,6 +1124,7 @@ static int64_t make_plan(const AttnArgs& a, Plan& p) {
     p.few_units = (uint32_t)few_units;
     p.many_units = (uint32_t)many_units;
     p.by_heads = FastDiv::of((uint32_t)hk);
+    p.by_few_chunk = FastDiv::of((uint32_t)p.few_chunk);
     p.by_few_parts = FastDiv::of((uint32_t)p.few_parts);
     if (p.pre_tiles) p.by_pre_tiles = FastDiv::of((uint32_t)p.pre_tiles);
     if (many) p.by_many_tiles = FastDiv::of((uint32_t)p.many_tiles);
@@ -1091,8 +1144,8 @@ size_t attn_workspace(const AttnArgs& a) {
 template <int DP, bool BF16, bool FP8>
 static hipError_t launch_one(const KArgs& ka, int64_t units) {
     if (plan_recorder()) {
-        plan_record("attn<%d,%s,%s> grid=%lld prefix=%d few=%d many=%d joint=%d", DP, BF16 ? "bf16" : "fp16", FP8 ? "e4m3" : "16",
-                    (long long)units, ka.p.pre_parts, ka.p.few_parts, ka.p.many_parts, (int)ka.p.joint);
+        plan_record("attn<%d,%s,%s> grid=%lld prefix=%d few=%d many=%d joint=%d listed=%d", DP, BF16 ? "bf16" : "fp16", FP8 ? "e4m3" : "16",
+                    (long long)units, ka.p.pre_parts, ka.p.few_parts, ka.p.many_parts, (int)ka.p.joint, (int)ka.p.listed);
         return hipSuccess;
     }
     hipLaunchKernelGGL((attn_kernel<DP, BF16, FP8>), dim3((unsigned)units), dim3(kThreads), 0, ka.a.stream, ka);

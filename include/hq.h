@@ -574,10 +574,11 @@ typedef struct hq_rope_desc {
  *   (softcap 0: c(x) = x).
  * q_heads: a multiple of kv_heads; query head h reads key head h / (q_heads /
  * kv_heads).  max_new and max_kv bound every request's new tokens and own
- * length; they and total_kv size the launch.  If they are too small, a request's
- * tokens from max_new on have no defined result, and its own keys from max_kv on
- * are not seen; larger ones only cost idle workgroups.  total_kv is the sum of
- * the own lengths if the caller knows it (a hint), else 0.
+ * length, and total_kv is the sum of the own lengths if the caller knows it, else
+ * 0; they size the launch.  Larger ones only cost idle workgroups.  If they are
+ * too small, a request's tokens from max_new on have no defined result, its own
+ * keys from max_kv on are not seen, and with a total_kv that is too small the last
+ * requests have no defined result.
  */
 typedef struct hq_attn_desc {
     int32_t abi_version; /* HQ_ABI_VERSION                                 */

@@ -281,3 +281,29 @@ def test_bounds_smaller_than_the_lengths(prefix):
     o2, l2, p2 = okv.attention(c.q[1:51].double().numpy(), lambda r: k, lambda r: v, prefix, [64 + 49], [0, 50], float(np.float32(c.scale)))
     t2, _ = c.bounds(o2, l2, p2)
     assert (np.abs(got[1:51] - o2) <= t2).all()
+
+
+def listed(c, **bounds):
+    from bit_quantized_gemm_w4a16_amd import hq
+    d, kv = c.descs(**bounds)
+    return "listed=1" in hq.hq_attn_plan(d, kv, len(c.new), c.total, c.prefix)[0]
+
+
+@pytest.mark.parametrize("B,Hq,Hk,D,dtype,cache,prefix,drafts", [
+    (7, 8, 2, 64, "bf16", "bf16", 0, 1), (64, 8, 2, 64, "fp16", "fp16", 300, 1), (65, 4, 4, 80, "bf16", "fp8", 0, 9), (200, 8, 1, 64, "bf16", "bf16", 0, 6),
+    (20, 16, 2, 128, "bf16", "bf16", 1000, 8), (40, 16, 2, 64, "bf16", "bf16", 100, 20), (130, 4, 1, 256, "fp16", "fp8", 77, 12)])
+def test_listed_parts(B, Hq, Hk, D, dtype, cache, prefix, drafts):
+    """Lengths that differ, known in sum: the parts are listed on the card.  Requests without new
+    tokens, without keys, with one or two tiles of rows, and with more than those hold."""
+    note(f"attn listed {B} {Hq}/{Hk} {D} {cache} prefix {prefix}")
+    g = np.random.default_rng(B)
+    held = g.integers(0, 60, B)
+    held[g.integers(0, B, max(B // 16, 1))] = 5000
+    held[B // 2], held[-1] = 0, 4999
+    new = g.integers(0, drafts + 1, B)
+    new[B // 2], new[-1], new[0] = drafts, 1, 0
+    c = AttnCase(held.tolist(), new.tolist(), Hq, Hk, D, dtype, cache=cache, prefix=prefix, seed=B)
+    total = int(sum(c.kv_lens))
+    assert listed(c, total_kv=total) and not listed(c)
+    c.check(total_kv=total)
+    c.check(total_kv=total + 1000)
