@@ -71,7 +71,8 @@ class ServedBlock:
     def share_prefix(self, x):
         """Runs the prompt that all requests share (request 0 of an otherwise empty
         block) and keeps its pages as the prefix."""
-        assert not any(self.lens) and not self.prefix_len and x.shape[0]
+        if any(self.lens) or self.prefix_len:
+            raise ValueError("a prefix is shared before all else")
         out = self.step(x, [x.shape[0]])
         self.prefix_len = x.shape[0]
         self.prefix_table.copy_(self.blocks[0])
@@ -80,10 +81,28 @@ class ServedBlock:
         self.lens = [0] * len(self.lens)
         return out
 
+    def admit(self, x, new):
+        """Refuses a step that the buffers do not hold, before anything is launched or
+        changed (the library is given addresses: it cannot tell).  Returns the lengths
+        after the step and the pages that it takes."""
+        T, hidden, context = sum(new), self.qkv.K, self.table.shape[0]
+        if (any(n < 0 for n in new) or tuple(x.shape) != (T, hidden) or x.dtype != torch.bfloat16 or not x.is_contiguous()
+                or x.device != self.positions.device):
+            raise ValueError(f"x must be a contiguous bf16 [{T}][{hidden}] beside the cache: a row for each new token")
+        if not 0 < T <= self.positions.numel() or len(new) > len(self.lens):
+            raise ValueError(f"{T} tokens of {len(new)} requests: from 1 to {self.positions.numel()} tokens of up to {len(self.lens)} requests fit")
+        after = [c + n for c, n in zip(self.lens, new)]
+        if self.prefix_len + max(after) > context:
+            raise ValueError(f"a request of {max(after)} tokens behind a prefix of {self.prefix_len} exceeds the context of {context}")
+        taken = sum(-(-k // self.block) - -(-c // self.block) for c, k in zip(self.lens, after))
+        if taken > self.free.numel():
+            raise ValueError(f"out of pages: {taken} needed, {self.free.numel()} free")
+        return after, taken
+
     def step(self, x, new):
         """x: hidden states [sum(new)][hidden] of new[r] new tokens of request r."""
         B, T, dt = len(new), x.shape[0], hq.HQ_DT_BF16
-        assert T == sum(new) and T > 0
+        after, taken = self.admit(x, new)
         fresh = torch.tensor(new, dtype=torch.int32, device="cuda")
         hq.hq_kv_slots(self.block, B, T, self.cached, fresh, self.free, self.free.numel(), self.blocks, self.max_blocks, self.cu, self.kv_lens,
                        self.positions, self.slots, self.taken, first_pos=self.prefix_len)
@@ -91,18 +110,15 @@ class ServedBlock:
         k, v = self.x_qkv[:, self.q_row:], self.x_qkv[:, self.q_row + self.kv_heads * self.head_dim:]
         hq.hq_rope_kv(self.rope, self.kv, dt, T, self.q_heads, self.x_qkv, self.row, k, self.row, v, self.row, self.positions, self.table,
                       self.table.shape[0], self.slots, self.q, self.q_row, self.k_cache, self.v_cache, self.k_scale, self.v_scale)
-        # the host knows the lengths too: it uses them to size the launch and to count the pages
-        before = self.lens[:B]
-        self.lens[:B] = [c + n for c, n in zip(before, new)]
-        desc = hq.attn_desc(dt, self.q_heads, max(new), max(self.lens[:B]), self.head_dim ** -0.5, total_kv=sum(self.lens[:B]))
+        # the host knows the lengths too: it uses them to size the launch
+        desc = hq.attn_desc(dt, self.q_heads, max(new), max(after), self.head_dim ** -0.5, total_kv=sum(after))
         need = hq.hq_attn_workspace_bytes(desc, self.kv, B, T, self.prefix_len)
         if need > self.workspace.numel():
             self.workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
         hq.hq_attn(desc, self.kv, B, T, self.q, self.q_row, self.k_cache, self.v_cache, self.prefix_table, self.prefix_len, self.blocks,
                    self.max_blocks, self.kv_lens, self.cu, self.heads, self.q_row, None, self.workspace, self.workspace.numel(), self.k_scale,
                    self.v_scale)
-        taken = sum(-(-(c + n) // self.block) - -(-c // self.block) for c, n in zip(before, new))
-        assert taken <= self.free.numel(), "out of pages"
+        self.lens[:B] = after
         self.free = self.free[taken:]
         self.cached[:B].copy_(self.kv_lens[:B])
         out = torch.empty(T, self.proj.N, dtype=torch.bfloat16, device="cuda")
