@@ -1166,7 +1166,7 @@ hipError_t attn_launch(const AttnArgs& a) {
     if (units < 1) return hipErrorInvalidConfiguration;
     ka.G = a.q_heads / a.kv.kv_heads;
     ka.per_group = FastDiv::of((uint32_t)ka.G);
-    if (ka.p.parts > 1) {
+    if (ka.p.parts > 1 && !plan_recorder()) {  // (a plan has no workspace to lay out)
         const size_t rows = (size_t)a.T * a.q_heads;
         char* w = (char*)a.ws;
         ka.part_o = (float*)w;
