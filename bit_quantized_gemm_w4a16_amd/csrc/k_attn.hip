@@ -1042,7 +1042,7 @@ static int64_t make_plan(const AttnArgs& a, Plan& p) {
     // 256 of 200 behind 128, 134 MB: 45.7, 48.4; behind 256, 267 MB: 50.6, 48.6).
     if (P > 0)
         p.joint = a.B == 1 || rows >= a.B * 16 * kRowsWide ||
-                  (P + a.max_kv <= chunk_of(P) && P * (a.B - 1) * hk * a.kv.head_dim * 2 * bytes <= (int64_t)128 << 20);
+                  (P + a.max_kv <= chunk_of(P) && P * (a.B - 1) * hk <= ((int64_t)128 << 20) / (a.kv.head_dim * 2 * bytes));
     const int64_t extra = p.joint ? P : 0, pre_keys = p.joint ? 0 : P;
     const int64_t longest = a.max_kv + extra > 0 ? a.max_kv + extra : 1, per = chunk_of(extra);
     auto split = [&](int64_t keys, int64_t per, int64_t step, int& chunk, int& parts) {  // equal chunks of about `per` keys

@@ -14,7 +14,7 @@ import pytest
 from test_sanitizers import CSRC, HIPCC, OUT, ROOT, _asan_runtime, _host_flags, _run
 
 HOST = ("hq_api.cpp", "hq_repack.cpp", "k_attn.hip")
-SUITES = ["tests/test_kv_host.py"]
+SUITES = ["tests/test_kv_host.py", "tests/test_kv_plan_host.py"]
 
 
 def _build() -> str:
