@@ -39,7 +39,13 @@ constexpr int kMaxParts = 256;                  // of the prefix, and of a reque
 constexpr int kAll = 0x7FFFFFFF;                // lim0: every row sees every key
 constexpr int kRun = 16;                        // keys of a run, see Stream
 constexpr float kNone = -3.0e38f;               // running maximum before any key
-constexpr float kSlack = 8.f;                   // weights stay below 2^kSlack
+constexpr float kSlack = 8.f;                   // weights stay below 2^kSlack (kLift higher in fp16)
+// Weights are taken against the maximum less kLift.  fp16 has steps of 2^-24 below
+// 2^-14: with the largest weight held as 1, those below 2^-25 of it would be lost
+// to the value product and still be in l.  Held as 2^7 (2^15 with the slack, fp16
+// ends at 2^16), only weights below 2^-32 of it are.  bf16 has fp32's range.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // How a call is cut into workgroups.  Three kinds of work in one launch:
@@ -267,7 +273,7 @@ struct Rows {
         float mx = st[0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) mx = fmaxf(mx, st[i]);
-        mx = fmaxf(mx, other_half(mx)) * c2;
+        mx = __builtin_fmaf(fmaxf(mx, other_half(mx)), c2, -kLift<BF16>);
         // The maximum that the weights are taken against only has to keep them in
         // range: it moves, and the sums with it, once it is behind by 2^kSlack.
         if (__any(mx > m + kSlack)) {
@@ -281,8 +287,10 @@ struct Rows {
         }
     }
     // Weights of the 32 keys, rounded to 16 bits as the operands of the value
-    // product (relative error up to 2^-8 or 2^-11 each, like the output's own);
-    // their sum is of the unrounded ones.
+    // product: a relative error of up to 2^-8 (bf16) or 2^-11 (fp16) each, like the
+    // output's own, and of up to 2^-32 of the row's largest weight for fp16 weights
+    // below 2^-21 of it; their sum is of the unrounded ones.  Weights held in two
+    // 16-bit parts would take half as many matrix instructions again.
     __device__ __forceinline__ void weights(const v16f& st, Frag8 (&p)[2]) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
