@@ -160,6 +160,16 @@ struct Keys {
     }
 };
 
+// What a workgroup does.
+struct Task {
+    Keys keys;
+    int kvh, nrows, row0, k0, k1, lim0, part;
+    int64_t tok0;
+    bool direct;
+    // keys below k1 that the rows of token `rtok`, counted from tok0, see
+    __device__ __forceinline__ int seen_by(int rtok) const { return min(k1, lim0 == kAll ? k1 : max(keys.shared, lim0 + rtok)); }
+};
+
 #if defined(__HIP_DEVICE_COMPILE__)
 __device__ __forceinline__ v2u tr16(lds_char* p) { return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)p)); }
 __device__ __forceinline__ v2u tr8(lds_char* p) { return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i)p)); }
@@ -210,27 +220,26 @@ struct Rows {
     bool live;
 
     // s = c2 x.k, or with a cap s = c2 tanh(y), tanh(y) = 1 - 2 / (1 + 2^(c1 x.k))
-    __device__ __forceinline__ void init(const KArgs& ka, const Keys& keys, int kvh, int64_t tok0, int nrows, int wrow0, int k1, int lim0) {
+    __device__ __forceinline__ void init(const KArgs& ka, const Task& w, int wrow0) {
         const AttnArgs& a = ka.a;
         const int D = a.kv.head_dim;
         lane = threadIdx.x & 63;
         half = lane >> 5;
         col = lane & 31;
         const int row = wrow0 + col;
-        live = row < nrows;
+        live = row < w.nrows;
         const int rtok = live ? (int)ka.per_group.div(row) : 0;
-        const int64_t tok = tok0 + rtok;
-        const int head = kvh * ka.G + (live ? row - rtok * ka.G : 0);
-        const int wtok = (int)ka.per_group.div(wrow0 < nrows ? wrow0 : 0);
-        seen = min(k1, lim0 == kAll ? k1 : max(keys.shared, lim0 + rtok));
-        wseen = __builtin_amdgcn_readfirstlane(min(k1, lim0 == kAll ? k1 : max(keys.shared, lim0 + wtok)));
+        const int64_t tok = w.tok0 + rtok;
+        const int head = w.kvh * ka.G + (live ? row - rtok * ka.G : 0);
+        seen = w.seen_by(rtok);
+        wseen = __builtin_amdgcn_readfirstlane(w.seen_by((int)ka.per_group.div(wrow0 < w.nrows ? wrow0 : 0)));
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const int d = dim_of(s);
             q[s].u = v4u{0u, 0u, 0u, 0u};
             if (live && d < D) q[s].u = ld16((const uint16_t*)a.q + tok * a.q_stride + (int64_t)head * D + d);
         }
-        const float ksc = FP8 ? a.k_scale[kvh] : 1.f;
+        const float ksc = FP8 ? a.k_scale[w.kvh] : 1.f;
         cap = a.softcap > 0.f;
         c1 = cap ? 2.f * kLog2e * a.scale * ksc / a.softcap : 0.f;
         c2 = cap ? a.softcap * kLog2e : a.scale * ksc * kLog2e;
@@ -398,33 +407,27 @@ struct Rows {
 };
 
 // Four elements of a row's result, or of its partial one (m, l and the sum of
-// weight times value), to where they belong.
+// weight times value), to where they belong.  A row that sees no key is 0; one
+// that sees keys, whose scores are all minus infinity, has l = 0 too and is NaN.
 template <bool BF16, bool FP8>
-__device__ __forceinline__ void put(const KArgs& ka, int kvh, int64_t tok0, int row, int d, v4f o, float m, float l, int part, bool direct) {
+__device__ __forceinline__ void put(const KArgs& ka, const Task& w, int row, int d, v4f o, float m, float l) {
     const AttnArgs& a = ka.a;
-    const int D = a.kv.head_dim, rt = (int)ka.per_group.div(row), head = kvh * ka.G + row - rt * ka.G;
-    const int64_t tok = tok0 + rt, at = tok * a.q_heads + head;
-    float f = FP8 ? a.v_scale[kvh] : 1.f;
-    if (direct) {
-        f = l > 0.f || l != l ? f / l : 0.f;
+    const int D = a.kv.head_dim, rt = (int)ka.per_group.div(row), head = w.kvh * ka.G + row - rt * ka.G;
+    const int64_t tok = w.tok0 + rt, at = tok * a.q_heads + head;
+    float f = FP8 ? a.v_scale[w.kvh] : 1.f;
+    if (w.direct) {
+        if (l == 0.f && w.seen_by(rt) > 0) l = __builtin_nanf("");
+        f = l == 0.f ? 0.f : f / l;
         *(uint2*)((uint16_t*)a.out + tok * a.out_stride + (int64_t)head * D + d) = make_uint2(pack2<BF16>(o[0] * f, o[1] * f), pack2<BF16>(o[2] * f, o[3] * f));
         if (d == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
     } else {
-        *(v4f*)(ka.part_o + ((int64_t)part * a.T * a.q_heads + at) * D + d) = o * f;
+        *(v4f*)(ka.part_o + ((int64_t)w.part * a.T * a.q_heads + at) * D + d) = o * f;
         if (d == 0) {  // a row's parts side by side
-            ka.part_m[at * ka.p.parts + part] = m;
-            ka.part_l[at * ka.p.parts + part] = l;
+            ka.part_m[at * ka.p.parts + w.part] = m;
+            ka.part_l[at * ka.p.parts + w.part] = l;
         }
     }
 }
-
-// What a workgroup does.
-struct Task {
-    Keys keys;
-    int kvh, nrows, row0, k0, k1, lim0, part;
-    int64_t tok0;
-    bool direct;
-};
 
 // ---------------------------------------------------------------------------
 // keys on their way to LDS
@@ -595,7 +598,7 @@ __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_c
     constexpr int STEP = kWaves * 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Rows<DP, BF16, FP8> x;
-    x.init(ka, w.keys, w.kvh, w.tok0, w.nrows, w.row0, w.k1, w.lim0);
+    x.init(ka, w, w.row0);
     S in(ka.a, w.keys, w.kvh, w.k1);
     lds_char* const wk = sk + wave * NS * TILE;  // this wave's tiles
     lds_char* const wv = sv + wave * NS * TILE;
@@ -673,7 +676,7 @@ __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_c
             l += f * s_l[v][r];
             o += f * *(const lds_v4f*)((lds_float*)(v < 2 ? sk : sv) + ((v & 1) * kCols + r) * R::kPitch + d);
         }
-        put<BF16, FP8>(ka, w.kvh, w.tok0, w.row0 + r, d, o, m, l, w.part, w.direct);
+        put<BF16, FP8>(ka, w, w.row0 + r, d, o, m, l);
     }
 }
 
@@ -695,9 +698,9 @@ __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_
     const int wrow0 = w.row0 + wave * kCols;
     const bool wlive = wrow0 < w.nrows;
     Rows<DP, BF16, FP8> x;
-    x.init(ka, w.keys, w.kvh, w.tok0, w.nrows, wrow0, w.k1, w.lim0);
+    x.init(ka, w, wrow0);
     // keys that every row of the workgroup sees
-    const int gseen = min(w.k1, w.lim0 == kAll ? w.k1 : max(w.keys.shared, w.lim0 + (int)ka.per_group.div(w.row0)));
+    const int gseen = w.seen_by((int)ka.per_group.div(w.row0));
     S in(ka.a, w.keys, w.kvh, w.k1);
     lds_char* const wk = sk + wave * 16 * S::B;  // this wave's rows of a tile
     lds_char* const wv = sv + wave * 16 * S::B;
@@ -775,7 +778,7 @@ __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_
 #pragma unroll 4
     for (int i = x.lane; i < rows * (DP / 4); i += 64) {
         const int r = i / (DP / 4), d = i % (DP / 4) * 4;
-        if (d < ka.a.kv.head_dim) put<BF16, FP8>(ka, w.kvh, w.tok0, wrow0 + r, d, *(const lds_v4f*)(o + r * R::kPitch + d), s_m[wave][r], s_l[wave][r], w.part, w.direct);
+        if (d < ka.a.kv.head_dim) put<BF16, FP8>(ka, w, wrow0 + r, d, *(const lds_v4f*)(o + r * R::kPitch + d), s_m[wave][r], s_l[wave][r]);
     }
 }
 
@@ -995,7 +998,9 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KArgs ka, int rpw, 
     }
     const int64_t tok = row / a.q_heads, hd = row - tok * a.q_heads;
     if (s || row >= rows || tok >= end) return;
-    const float l = s_l[sub], inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    float l = s_l[sub];
+    if (l == 0.f && n > 0) l = __builtin_nanf("");  // it sees keys: see put
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     *(uint2*)((uint16_t*)a.out + tok * a.out_stride + hd * D + 4 * d4) = make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
     if (a.lse && d4 == 0) a.lse[row] = l == 0.f ? -INFINITY : (s_m[sub] + __builtin_amdgcn_logf(l)) * kLn2;
 }

@@ -658,7 +658,8 @@ hq_status hq_rope_kv(const hq_rope_desc* rope, const hq_kv_desc* kv, int32_t dty
  *              cu_new [B+1]
  *   k_scale, v_scale  fp32 [kv_heads] for an E4M3 cache, else NULL
  *   lse        fp32 [T][q_heads] or NULL: log sum_j exp(c(scale q.k_j))
- * A token that sees no key gets out = 0 and lse = -inf.  Keys that a token does
+ * A token that sees no key gets out = 0 and lse = -inf; one whose scores are all
+ * -inf has no softmax and gets NaN.  Keys that a token does
  * not see never reach it, whatever they hold (NaN and infinities included);
  * bytes of the cache beyond the lengths are not read.  Pages outside the cache
  * read as zeros.  Rows at and past cu_new[B] are not written.  Products take

@@ -1,5 +1,5 @@
 """GPU attention at values where roundings or infinities decide: long flat tails
-behind one strong key."""
+behind one strong key, rows whose scores are all minus infinity."""
 import numpy as np
 import pytest
 import torch
@@ -54,3 +54,39 @@ def test_flat_tail_keeps_its_mass_in_fp16(lens, new, cache):
     err = np.abs(got - out)
     assert (err <= tol).all(), float((err / tol).max())
     assert (np.abs(ls - lse) <= es + 2.0 ** -20 + (seen + 64) * 2.0 ** -24).all()
+
+
+# ---------------------------------------------------------------------------
+# scores of minus infinity
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("lens,new,prefix", [([300], [1], 0), ([4000], [1], 0), ([200], [120], 0), ([4000, 1500, 1500], [1, 40, 3], 900)])
+def test_rows_whose_scores_are_all_minus_infinity(dtype, lens, new, prefix):
+    """A row that sees keys, all of weight 0 / 0, has no softmax: NaN, as the formula gives, and not
+    the zeros of a row that sees none.  One finite score among them takes all the weight."""
+    note(f"attn minus infinity {dtype} {lens} prefix {prefix}")
+    c = AttnCase(lens, new, 4, 1, 64, dtype, prefix=prefix, seed=2)
+    c.q[..., 0] = 1.0
+    c.store[0][..., 0] = -float("inf")
+    got, ls, _ = c.run()
+    assert np.isnan(got).all() and np.isnan(ls).all()
+    b, s = place(c, 0, 0, 77)  # of the first request: its tokens that see it
+    c.store[0][b, s, 0, 0] = 0.0
+    got, ls, _ = c.run()
+    out, lse, _ = c.oracle()
+    assert np.array_equal(np.isnan(got), np.isnan(out)) and np.array_equal(np.isnan(ls), np.isnan(lse))
+    seen = ~np.isnan(lse)
+    assert seen.any()
+    np.testing.assert_array_equal(got[seen], out[seen])  # one key's value, held in the output's type
+    assert (np.abs(ls[seen] - lse[seen]) <= 2.0 ** -20 * (1 + np.abs(lse[seen]))).all()
+
+
+def test_rows_without_keys_next_to_rows_of_minus_infinity():
+    note("attn minus infinity, no keys")
+    c = AttnCase([2, 40], [5, 1], 4, 2, 64, "bf16", seed=1)
+    c.q[..., 0] = 1.0
+    c.store[0][..., 0] = -float("inf")
+    got, ls, _ = c.run()
+    assert (got[:3] == 0).all() and np.isneginf(ls[:3]).all()
+    assert np.isnan(got[3:]).all() and np.isnan(ls[3:]).all()
