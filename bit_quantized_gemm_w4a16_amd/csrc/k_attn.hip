@@ -46,6 +46,7 @@ constexpr float kSlack = 8.f;                   // weights stay below 2^kSlack (
 // ends at 2^16), only weights below 2^-32 of it are.  bf16 has fp32's range.
 template <bool BF16>
 constexpr float kLift = BF16 ? 0.f : 7.f;
+constexpr float kWideCap = 64.f;                // caps above it have kernels of their own, see Rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // How a call is cut into workgroups.  Three kinds of work in one launch:
@@ -207,19 +208,24 @@ __device__ __forceinline__ v16f mfma32(const Frag8& a, const Frag8& b, v16f c) {
 // row col's statistics and its output elements 32 t + 8 (i / 4) + 4 half + i % 4
 // (register i of tile t).  Scores come as registers of keys
 // kb + 8 (i / 4) + 4 half + i % 4.
-template <int DP, bool BF16, bool FP8>
+template <int DP, bool BF16, bool FP8, bool WIDE>
 struct Rows {
     static constexpr int KS = DP / 16, DT = DP / 32;
     Frag8 q[KS];
     v16f acc[DT];
     float m, l;
-    float c1, c2;
+    float c1, c2, cy, inv;
     bool cap;
     int half, col, lane;
     int seen, wseen;  // keys that this lane's row sees; that every row of the wave sees
     bool live;
 
-    // s = c2 x.k, or with a cap s = c2 tanh(y), tanh(y) = 1 - 2 / (1 + 2^(c1 x.k))
+    // s = c2 x.k, or with a cap s = c2 tanh(y), y = cy x.k.  tanh_far errs by 2^-22 of
+    // the cap: up to kWideCap less than 2^-16 of a weight, far below its rounding.
+    // Beyond that it would show, and small y go by the series, whose error is a share
+    // of the score: s = c2 (x.k) (tanh(y) / y).  These are kernels of their own (WIDE):
+    // 40 requests of drafts and a prompt chunk, cap 30, take 31 us, 38 by the series,
+    // and 37 where one kernel holds both ways; prompts without a cap 513 instead of 501.
     __device__ __forceinline__ void init(const KArgs& ka, const Task& w, int wrow0) {
         const AttnArgs& a = ka.a;
         const int D = a.kv.head_dim;
@@ -241,8 +247,10 @@ struct Rows {
         }
         const float ksc = FP8 ? a.k_scale[w.kvh] : 1.f;
         cap = a.softcap > 0.f;
-        c1 = cap ? 2.f * kLog2e * a.scale * ksc / a.softcap : 0.f;
-        c2 = cap ? a.softcap * kLog2e : a.scale * ksc * kLog2e;
+        c2 = (cap && !WIDE ? a.softcap : a.scale * ksc) * kLog2e;
+        cy = cap ? fminf(a.scale * ksc / a.softcap, 1e30f) : 0.f;  // (finite: 0 times it is 0)
+        c1 = 2.f * kLog2e * cy;
+        inv = cap ? a.softcap / (a.scale * ksc) : 0.f;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -261,16 +269,27 @@ struct Rows {
     // 8-bit cache are one load).
     __device__ __forceinline__ int dim_of(int s) const { return 32 * (s >> 1) + 16 * half + 8 * (s & 1); }
 
+    // tanh(y) of 2^t = e^2y, to some 2^-22 of 1; and tanh(y) / y of z = y^2 < 1/16, to
+    // 2^-22 of itself (the next term is 2^-27).
+    __device__ __forceinline__ static float tanh_far(float t) { return 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t)); }
+    __device__ __forceinline__ static float tanh_series(float z) {
+        return __builtin_fmaf(z, __builtin_fmaf(z, __builtin_fmaf(z, __builtin_fmaf(z, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+    }
     // Scores of keys kb..kb+31: cap and mask, and the running maximum.
     __device__ __forceinline__ void prepare(v16f& st, int kb) {
         // (in the two uniform branches a value passes through an empty asm, so that
         // nothing is computed ahead of the branch)
-        if (cap) {
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float y = cy * st[i], z = y * y;
+                st[i] = z < 0.0625f ? st[i] * tanh_series(z) : inv * tanh_far(c1 * st[i]);
+            }
+        } else if (cap) {
             float c = c1;
             asm volatile("" : "+v"(c));
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                st[i] = 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(c * st[i]));
+            for (int i = 0; i < 16; ++i) st[i] = tanh_far(c * st[i]);
         }
         if (kb + 32 > wseen) {
             int over = seen - kb - 4 * half;
@@ -591,13 +610,13 @@ constexpr int kStages = FP8 ? 2 : 1;
 // all the time both are on their way.  64 requests of 4096 keys, 64/8 heads of
 // 128: 5.4 TB/s in 16 bits, 4.6 in 8, where a large copy reaches 5.2.  The waves
 // are joined at the end.
-template <int DP, bool BF16, bool FP8>
+template <int DP, bool BF16, bool FP8, bool WIDE>
 __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_char* sk, lds_char* sv) {
     typedef Stream<DP, FP8, 32> S;
     constexpr int NL = S::NL, NS = kStages<FP8>, TILE = 32 * S::B;
     constexpr int STEP = kWaves * 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    Rows<DP, BF16, FP8> x;
+    Rows<DP, BF16, FP8, WIDE> x;
     x.init(ka, w, w.row0);
     S in(ka.a, w.keys, w.kvh, w.k1);
     lds_char* const wk = sk + wave * NS * TILE;  // this wave's tiles
@@ -652,7 +671,7 @@ __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_c
     // The waves' results meet in LDS, and all threads join them, four elements at
     // a time (in a loop, and only the rows there are: with few keys a workgroup's
     // time is the latency of code that it runs once).
-    typedef Rows<DP, BF16, FP8> R;
+    typedef Rows<DP, BF16, FP8, WIDE> R;
     __shared__ float s_m[kWaves][kCols], s_l[kWaves][kCols];
     if (x.half == 0) {
         s_m[wave][x.col] = x.m;
@@ -690,14 +709,14 @@ __device__ __forceinline__ void attend_few(const KArgs& ka, const Task& w, lds_c
 // it turns the last ones into weights.  A wave fetches 16 rows of each tile; K of
 // the tile after the next goes where this tile's was once all have read it, half
 // a tile before V does, so each has a whole tile's time to arrive.
-template <int DP, bool BF16, bool FP8>
+template <int DP, bool BF16, bool FP8, bool WIDE>
 __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_char* sk, lds_char* sv) {
     typedef Stream<DP, FP8, 16> S;
     constexpr int KT = 64, NL = S::NL, TILE = KT * S::B, HALF = 32 * S::B;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wrow0 = w.row0 + wave * kCols;
     const bool wlive = wrow0 < w.nrows;
-    Rows<DP, BF16, FP8> x;
+    Rows<DP, BF16, FP8, WIDE> x;
     x.init(ka, w, wrow0);
     // keys that every row of the workgroup sees
     const int gseen = w.seen_by((int)ka.per_group.div(w.row0));
@@ -765,7 +784,7 @@ __device__ __forceinline__ void attend_many(const KArgs& ka, const Task& w, lds_
     x.l += other_half(x.l);
     if (__syncthreads_or(bad) && wlive) x.add_nonfinite(ka, w.keys, w.kvh, gseen < w.k0 ? w.k0 : w.k0 + (gseen - w.k0) / KT * KT, w.k0, w.k1, 1, 0);
     // each wave's rows through its own share of the tiles' LDS, so that whole rows are written
-    typedef Rows<DP, BF16, FP8> R;
+    typedef Rows<DP, BF16, FP8, WIDE> R;
     __shared__ float s_m[kWaves][kCols], s_l[kWaves][kCols];
     if (x.half == 0) {
         s_m[wave][x.col] = x.m;
@@ -850,11 +869,11 @@ __device__ __forceinline__ bool find_few(const KArgs& ka, int unit, int& r, int&
     return false;
 }
 
-template <int DP, bool BF16, bool FP8>
+template <int DP, bool BF16, bool FP8, bool WIDE>
 __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(KArgs ka) {
     // two tiles of 64 rows of K and of V, or the four waves' tiles of 32 (8 bits:
     // twice two); then the results of two waves in each
-    constexpr int kTiles = 2 * 64 * DP * 2, kResults = 2 * kCols * Rows<DP, BF16, FP8>::kPitch * 4;
+    constexpr int kTiles = 2 * 64 * DP * 2, kResults = 2 * kCols * Rows<DP, BF16, FP8, WIDE>::kPitch * 4;
     __shared__ __attribute__((aligned(16))) char s_k[kTiles > kResults ? kTiles : kResults], s_v[kTiles > kResults ? kTiles : kResults];
     const AttnArgs& a = ka.a;
     const Plan& p = ka.p;
@@ -935,8 +954,8 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(KArgs
         k1 = (int)min(k0 + chunk, (int64_t)end);
     }
     const Task w{keys, kvh, rows, row0, (int)k0, k1, lim0, base + part, tok0, direct};
-    if (few) attend_few<DP, BF16, FP8>(ka, w, (lds_char*)s_k, (lds_char*)s_v);
-    else attend_many<DP, BF16, FP8>(ka, w, (lds_char*)s_k, (lds_char*)s_v);
+    if (few) attend_few<DP, BF16, FP8, WIDE>(ka, w, (lds_char*)s_k, (lds_char*)s_v);
+    else attend_many<DP, BF16, FP8, WIDE>(ka, w, (lds_char*)s_k, (lds_char*)s_v);
 }
 
 // Joins the parts of every row.  A workgroup takes `rpw` rows; the weights of
@@ -1156,12 +1175,14 @@ size_t attn_workspace(const AttnArgs& a) {
 
 template <int DP, bool BF16, bool FP8>
 static hipError_t launch_one(const KArgs& ka, int64_t units) {
+    const bool wide = ka.a.softcap > kWideCap;
     if (plan_recorder()) {
-        plan_record("attn<%d,%s,%s> grid=%lld prefix=%d few=%d many=%d joint=%d listed=%d", DP, BF16 ? "bf16" : "fp16", FP8 ? "e4m3" : "16",
-                    (long long)units, ka.p.pre_parts, ka.p.few_parts, ka.p.many_parts, (int)ka.p.joint, (int)ka.p.listed);
+        plan_record("attn<%d,%s,%s%s> grid=%lld prefix=%d few=%d many=%d joint=%d listed=%d", DP, BF16 ? "bf16" : "fp16", FP8 ? "e4m3" : "16",
+                    wide ? ",wide" : "", (long long)units, ka.p.pre_parts, ka.p.few_parts, ka.p.many_parts, (int)ka.p.joint, (int)ka.p.listed);
         return hipSuccess;
     }
-    hipLaunchKernelGGL((attn_kernel<DP, BF16, FP8>), dim3((unsigned)units), dim3(kThreads), 0, ka.a.stream, ka);
+    if (wide) hipLaunchKernelGGL((attn_kernel<DP, BF16, FP8, true>), dim3((unsigned)units), dim3(kThreads), 0, ka.a.stream, ka);
+    else hipLaunchKernelGGL((attn_kernel<DP, BF16, FP8, false>), dim3((unsigned)units), dim3(kThreads), 0, ka.a.stream, ka);
     return hipGetLastError();
 }
 

@@ -1,5 +1,5 @@
 """GPU attention at values where roundings or infinities decide: long flat tails
-behind one strong key, rows whose scores are all minus infinity."""
+behind one strong key, rows whose scores are all minus infinity, caps of any size."""
 import numpy as np
 import pytest
 import torch
@@ -90,3 +90,34 @@ def test_rows_without_keys_next_to_rows_of_minus_infinity():
     got, ls, _ = c.run()
     assert (got[:3] == 0).all() and np.isneginf(ls[:3]).all()
     assert np.isnan(got[3:]).all() and np.isnan(ls[3:]).all()
+
+
+# ---------------------------------------------------------------------------
+# caps far above the scores
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("cache", ["fp16", "fp8"])
+@pytest.mark.parametrize("softcap", [0.5, 50.0, 1e4, 1e6, 1e12])
+@pytest.mark.parametrize("lens,new,prefix", [([300, 41], [1, 9], 50), ([3000, 900], [1, 2], 700), ([260], [130], 0)])
+def test_cap_errs_by_a_share_of_the_score(softcap, cache, lens, new, prefix):
+    """cap * tanh(x / cap) to 2^-19 of x, whatever the cap (tanh of a quarter and
+    more to some 2^-22, below that by its series)."""
+    note(f"attn cap {softcap} {cache} {lens} {prefix}")
+    c = AttnCase(lens, new, 8, 2, 64, "fp16", cache, prefix=prefix, softcap=softcap, q_gain=3.0, seed=2)
+    got, ls, _ = c.run()
+    out, lse, (mass, qk, seen, vmax) = c.oracle()
+    u = U["fp16"]
+    es = (2.0 ** -24 * (c.D + 8) + 2.0 ** -19) * qk + 2.0 ** -22 * (1 + np.abs(lse))
+    tol = (u + 2 * es + 2.0 ** -21 + (seen + 64) * 2.0 ** -24)[..., None] * mass + (seen * TINY["fp16"] * vmax)[..., None] + u * np.abs(out) + TINY["fp16"]
+    err = np.abs(got - out)
+    assert (err <= tol).all(), float((err / tol).max())
+    e2, ltol = np.abs(ls - lse), es + 2.0 ** -20 + (seen + 64) * 2.0 ** -24
+    assert (e2 <= ltol).all(), float((e2 / ltol).max())
+
+
+def test_cap_beyond_all_scores_changes_nothing():
+    note("attn cap 1e30")
+    a = AttnCase([300, 41], [1, 40], 8, 2, 64, "bf16", prefix=50, softcap=1e30, seed=2)
+    b = AttnCase([300, 41], [1, 40], 8, 2, 64, "bf16", prefix=50, seed=2)
+    x, y = a.run(), b.run()
+    assert np.array_equal(x[0], y[0]) and np.array_equal(x[1], y[1])
