@@ -53,7 +53,7 @@ struct KvSlotsArgs {
 hipError_t kv_slots_launch(const KvSlotsArgs& a);
 
 struct RopeTableArgs {
-    double turns[128];  // turns of one position step, per pair
+    double turns[128], rest[128];  // turns of one position step, per pair, in two parts
     double gain;
     int64_t first, count;
     int half;

@@ -150,21 +150,22 @@ hipError_t kv_slots_launch(const KvSlotsArgs& a) {
 // ---------------------------------------------------------------------------
 
 // A thread writes `run` consecutive positions of one pair: cos and sin of the
-// first in 64 bits (position * turns is exact to 2^-53 of its value; taking off
-// the nearest whole number of turns leaves at most half a turn, whatever the
-// position), then each next one by turning that by the pair's step, four 64-bit
-// operations, whose error after 32 steps is still below 2^-46; rounded once to
-// fp32.  A library cos and sin for each element was bound by arithmetic (131072
-// positions x 128 elements: 22 us); this is bound by the stores (11 to 12.6 us,
-// 5.3 to 6.1 TB/s; a large fill reaches 6.8).
+// first in 64 bits, then each next one by turning that by the pair's step, four
+// 64-bit operations, whose error after 32 steps is still below 2^-46; rounded once
+// to fp32.  The first's angle is position * (turns + rest) less the nearest whole
+// number of turns, by fma, so that the product is not rounded before that is
+// taken off: right to 2^-30 of a turn at the last position, 2^-46 at 131072.  A
+// library cos and sin for each element was bound by arithmetic (131072 positions
+// x 128 elements: 22 us); this is bound by the stores (11 to 12.6 us, 5.3 to 6.1
+// TB/s; a large fill reaches 6.8).
 __global__ __launch_bounds__(256) void rope_table_kernel(RopeTableArgs a, int run) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t row0 = i / a.half * run;
     if (row0 >= a.count) return;
     const int d = (int)(i - row0 / run * a.half);
-    const double turn = (double)(a.first + row0) * a.turns[d];
+    const double pos = (double)(a.first + row0), turn = fma(pos, a.turns[d], -rint(pos * a.turns[d]));
     double c, s, cs, ss;
-    sincospi(2.0 * (turn - rint(turn)), &s, &c);
+    sincospi(2.0 * fma(pos, a.rest[d], turn), &s, &c);
     sincospi(2.0 * a.turns[d], &ss, &cs);  // (fewer than half a turn: base > 1)
     const int64_t end = min(row0 + run, a.count);
     float* at = a.table + row0 * 2 * a.half + d;

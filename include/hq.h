@@ -619,8 +619,8 @@ hq_status hq_kv_slots(int32_t block_size, int64_t B, int64_t T_cap, int64_t max_
 
 /*
  * Rotary table rows first_pos .. first_pos + count - 1: fp32 [count][rot_dim],
- * cos of the rot_dim/2 angles, then their sin.  Angles are reduced in 64 bits,
- * so no position loses accuracy.  first_pos + count <= 2^31.
+ * cos of the rot_dim/2 angles, then their sin.  Angles are reduced in 64 bits
+ * from turns in two parts: right to 2^-30 of a turn at every position.  first_pos + count <= 2^31.
  */
 hq_status hq_rope_table(const hq_rope_desc* rope, int64_t first_pos, int64_t count, float* table, hq_stream_t stream);
 
