@@ -139,15 +139,27 @@ def _check(status: int, where: str):
         raise HQError(status, where, lib().hq_last_error().decode())
 
 
+# How a value of each type gives its address: told by the type alone, as isinstance for
+# each of the 13 tensors of a call costs 1 us, and an attribute that is not there 0.3 us.
+_address_of = {int: lambda t: t, np.ndarray: lambda t: t.ctypes.data}
+
+
 def _dp(t):
     """Device (or host numpy) pointer of a tensor/array; None -> NULL."""
     if t is None:
         return None
-    try:
-        ptr = t.data_ptr  # first: a call with 13 tensors takes 1 us less than with two isinstance before it
-    except AttributeError:
-        return t if isinstance(t, int) else t.ctypes.data
-    return ptr()
+    of = _address_of.get(type(t))
+    return of(t) if of else _first_address(t)
+
+
+def _first_address(t):
+    """Of the first value of its type: a tensor, or another kind of int or array."""
+    of = getattr(type(t), "data_ptr", None)
+    if of is None:
+        of = _address_of[int if isinstance(t, int) else np.ndarray]
+    ptr = of(t)
+    _address_of[type(t)] = of
+    return ptr
 
 
 _raw_stream = None  # gives the handle of torch's current stream
