@@ -902,37 +902,43 @@ def tune_table(work, log_fn=log):
                  gain=round(base / b, 3)) for M, (t, b, base) in table.items()]
 
 
-# The library's sources: counter figures taken on other versions of them are stale.
+# The sources that the quantized layers' kernels are built from.  Not those of the
+# paged-cache operators, and not hq_api.cpp and hq.h, which choose the launches: a
+# figure names its launch, and counts only where that is still the one planned.
+OTHER_SOURCES = ("k_attn.hip", "k_kv.hip", "hq_kv.h", "hq_api.cpp")
 KERNEL_SOURCES = sorted("bit_quantized_gemm_w4a16_amd/csrc/" + f
                         for f in os.listdir(os.path.join(ROOT, "bit_quantized_gemm_w4a16_amd", "csrc"))
-                        if f.endswith((".hip", ".hpp", ".h", ".cpp")))
-KERNEL_SOURCES += ["include/hq.h", "bit_quantized_gemm_w4a16_amd/build.py"]   # (the build flags shape the code too)
+                        if f.endswith((".hip", ".hpp", ".h", ".cpp")) and f not in OTHER_SOURCES)
+KERNEL_SOURCES += ["bit_quantized_gemm_w4a16_amd/build.py"]   # (the build flags shape the code too)
 
 
-def kernel_source_hash():
-    """Hash of the library's sources; counter figures taken on other sources are stale."""
+def kernel_source_hash(root=ROOT):
+    """Hash of the kernels' sources; counter figures taken on other sources are stale."""
     import hashlib
     h = hashlib.sha256()
     for f in KERNEL_SOURCES:
-        with open(os.path.join(ROOT, f), "rb") as fh:
+        with open(os.path.join(root, f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
 
 
-def _traffic(workload, M):
+def _traffic(work, M):
     """HBM bytes at M from the committed counter runs (profiles/traffic.json):
     FETCH_SIZE + WRITE_SIZE per dispatch, each scaled by the factor the same counter
     gives on a plain device copy of known size; `kernel_bytes` for one launch of the
     call's main kernel, `call_bytes` for all of the call's launches.  None when
-    absent or taken on other sources."""
+    absent, taken on other sources or of another launch than the one planned now."""
     path = os.path.join(ROOT, "profiles", "traffic.json")
     if not os.path.exists(path):
         return None
     with open(path) as fh:
-        rec = json.load(fh).get(workload)
+        rec = json.load(fh).get(work.name)
     if not rec or rec.get("source_hash") != kernel_source_hash():
         return None
-    return rec.get("per_M", {}).get(str(M))
+    row = rec.get("per_M", {}).get(str(M))
+    if row and not hasattr(work, "E") and row["kernel"] not in hq.hq_gemm_plan(work.desc, M):
+        return None
+    return row
 
 
 MEASURED = {}   # on-device peaks from the library's probes (filled by measure_peaks)
@@ -999,7 +1005,7 @@ def report(work, args, wall, per, cpu_budget=16.0):
                    mfma_frac=round(F / t / peak, 3), roofline_frac=round(max(B / PEAK_HBM, F / peak) / t, 3))
         if hasattr(work, "routing_us") and not args.eager:   # (eager: counter runs, no extra launches)
             row["routing_us"] = work.routing_us(M)
-        tr = _traffic(work.name, M)
+        tr = _traffic(work, M)
         if tr:   # HBM bytes of the whole call from the counter runs, against the algorithmic bytes
             row["traffic_bytes"] = tr["call_bytes"]
             row["traffic_ratio"] = round(tr["call_bytes"] / B, 3)
@@ -1026,7 +1032,7 @@ def report(work, args, wall, per, cpu_budget=16.0):
     if key in MEASURED:   # the same achieved rate against the probe-measured peak
         roof.update(measured_peak=round(MEASURED[key] / (1e9 if key == "hbm" else 1e12), 1),
                     frac_of_measured=round((B if key == "hbm" else F) / t / MEASURED[key], 4))
-    tr = _traffic(work.name, Mr)
+    tr = _traffic(work, Mr)
     roof.update(traffic=tr["kernel_bytes"] if tr else None, kernel=dom, M=Mr, avg_us=round(t * 1e6, 2),
                 algorithmic_flops=F, algorithmic_bytes=B,
                 per_unit="2*M*N*K flops per launch" if bound == "mfma" else "algorithmic bytes per launch")
