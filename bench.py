@@ -6,10 +6,12 @@ M in {1, 2, 4, ..., 8192} one library call (host dispatch -> HIP kernels ->
 output) on inputs already resident in HBM.  The headline workload is the
 dense W4A16 asymmetric layer (fp16 activations, UINT4 weights with UINT4
 zero-points and fp16 scales per 128 K, N=4096, K=7168), the configuration
-the metric is quoted on; its line also carries, under "configs", the same
-measurement of every other workload (dense W4A8-MXFP4, W8A8-INT8, the MoE
-gate-up on the Indexed path with its routing timed apart, W4A4 MXFP4 x MXFP4,
-MXFP8 x MXFP4, FP8 W8A8 with blockwise scales, bf16 x MXFP4, NVFP4 and MXINT4 WnA16, INT8 and FP8 weight-only).
+the metric is quoted on; its line also carries, under "configs", the result of
+the same measurement of every other workload (dense W4A8-MXFP4, W8A8-INT8, the
+MoE gate-up on the Indexed path with its routing timed apart, W4A4 MXFP4 x
+MXFP4, MXFP8 x MXFP4, FP8 W8A8 with blockwise scales, bf16 x MXFP4, NVFP4 and
+MXINT4 WnA16, INT8 and FP8 weight-only and the low-bit and wide layers);
+--details FILE writes every workload's record whole, with its rows per M.
 --config NAME measures one workload alone (c5g: the MoE Grouped path, c5l:
 the whole MoE layer the pages time, gate-up + SwiGLU + down).
 
@@ -1182,6 +1184,16 @@ def _ncopies(desc):
     return max(2, -(-COLD_BYTES // sum(hq.hq_repacked_bytes(desc))))
 
 
+def headline(head, extra):
+    """The default run's line: the headline workload's record whole, of each other one its
+    result (17 whole records made a line of 65 KB, which readers of lines cut)."""
+    short = {}
+    for nm, rec in extra.items():
+        short[nm] = {k: rec[k] for k in ("value", "unit", "ms_per_step", "dtype")}
+        short[nm].update(workload=rec["config"]["workload"], roofline_frac=rec["roofline"]["frac"], M=rec["roofline"]["M"])
+    return json.dumps({**head, "configs": short})
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -1198,6 +1210,8 @@ def main():
     ap.add_argument("--autotune", action="store_true",
                     help="also time every tuning override per M (dense workloads) and report the fastest")
     ap.add_argument("--no-peaks", action="store_true", help="skip the on-device peak probes")
+    ap.add_argument("--details", default=None, metavar="FILE",
+                    help="also write the default run's whole record to FILE: every workload's, with its rows per M")
     ap.add_argument("--copy-probe", type=int, default=0, metavar="BYTES",
                     help="only run a plain device copy of BYTES (counter calibration) and exit")
     ap.add_argument("--kernel-stats", default=None, metavar="CSV",
@@ -1243,12 +1257,11 @@ def main():
     if args.config is None:
         head = measure("c2", 16.0)
         head["peaks"] = peaks
-        head["configs"] = {}
-        for nm in DEFAULT_EXTRA:
-            rec = measure(nm, 3.0)
-            head["configs"][nm] = {k: rec[k] for k in ("value", "unit", "ms_per_step", "dtype", "config", "roofline",
-                                                       "cpu_baseline", "per_M") + (("aux",) if "aux" in rec else ())}
-        print(json.dumps(head), flush=True)
+        extra = {nm: measure(nm, 3.0) for nm in DEFAULT_EXTRA}
+        if args.details:
+            with open(args.details, "w") as fh:
+                json.dump({**head, "configs": extra}, fh)
+        print(headline(head, extra), flush=True)
         return
     names = list(WORKLOADS) if args.config == "all" else [args.config]
     for nm in names:
