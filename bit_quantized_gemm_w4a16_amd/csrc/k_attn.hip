@@ -1044,7 +1044,8 @@ static int64_t make_plan(const AttnArgs& a, Plan& p) {
     const int64_t bytes = a.kv.dtype == HQ_DT_FP8_E4M3 ? 1 : 2;
     const bool many = a.max_new * G > kFewTiles * kCols;
     const int64_t own_tiles = many ? cdiv(rows, kRowsWide) + a.B : a.B;
-    // Own keys of a workgroup.  The lengths are only known on the card, so chunks
+    // Own keys of a workgroup.  The lengths are only known on the card (where their
+    // sum is not given, every request counts with the bound of its length), so chunks
     // are equal, and two a slot rather than one even out requests of different
     // lengths (17 requests of 4k to 32k keys, 8 heads, E4M3: one 130 us, two 111,
     // four 129).  Where that gives 512 keys or fewer, a workgroup's time is latency.
@@ -1092,6 +1093,11 @@ static int64_t make_plan(const AttnArgs& a, Plan& p) {
         // and a join takes 8 us where there would be none (2 requests of 256 tokens at
         // 6000 keys, 32/8 heads: 78 us in 4 parts, 91 in 7; 3 prompts of some 440 up to
         // 1048 keys, 40/8, E4M3: 55 in one, 73 in 3; 4 of 64 at 700: 29 in one, 32 in 4).
+        // Every tile counts with the average length of all requests, and where one part
+        // is best here, the few rows of the others have one too, which leaves them no
+        // join.  Both hold where the others' keys are not many more: long decodes beside
+        // a chunk of a prompt are not cut (a chunk of 8192 tokens 599 us, a decode of
+        // 131072 keys, 32/8 heads of 128, 113; in one call 1529).
         int64_t best = 0, n = 1;
         const int64_t key = pad_dim(a.kv.head_dim) == 256 ? 70 : 35, avg = total / a.B + extra;
         const int64_t share = hk * avg * (rows / kRowsWide + cdiv(a.B, 2)) / slots;
@@ -1102,7 +1108,7 @@ static int64_t make_plan(const AttnArgs& a, Plan& p) {
             if (i == 1 || ns < best) best = ns, n = i;
         }
         split(longest, cdiv(longest, n), 64, p.many_chunk, p.many_parts);
-        whole = n == 1 && !pre_keys;  // the others' rows take less time for as many keys
+        whole = n == 1 && !pre_keys;
         p.many_tiles = (int)(rows / kRowsWide + a.B);
         many_units = group_units(hk * p.many_parts, p.many_tiles);
     }

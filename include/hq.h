@@ -550,7 +550,9 @@ typedef struct hq_kv_desc {
  *   PARTS   with t_d = context * f_d / (2 pi) turns in the trained context and
  *           g_d = clamp((t_d - slow) / (fast - slow), 0, 1):
  *           f_d * g_d + (f_d / factor) * (1 - g_d); cos and sin are multiplied
- *           by attn_factor (0: 0.1 ln(factor) + 1)
+ *           by attn_factor (0: 0.1 ln(factor) + 1).  The ramp is linear in
+ *           turns; a ramp that is linear in the pair's index d between bounds
+ *           made of slow and fast has other frequencies in between
  * rot_dim: a multiple of 16, 16..256.  base > 1; factor >= 1; PARTS: context
  * >= 1 and fast > slow.  Every kind but PARTS needs attn_factor 0.
  */
@@ -574,8 +576,12 @@ typedef struct hq_rope_desc {
  *   (softcap 0: c(x) = x).
  * q_heads: a multiple of kv_heads; query head h reads key head h / (q_heads /
  * kv_heads).  max_new and max_kv bound every request's new tokens and own
- * length, and total_kv is the sum of the own lengths if the caller knows it, else
- * 0; they size the launch.  Larger ones only cost idle workgroups.  If they are
+ * length, and total_kv is the sum of the own lengths (or bounds it) if the caller
+ * knows it, else 0; they size the launch and the workspace.  Larger ones give the
+ * same result but for the order of its sums, and take longer: with total_kv 0,
+ * every request is taken to be max_kv long, and workgroups get as many keys each
+ * as that asks for (8 requests of 4000 keys, 32/8 heads of 128: 29 us; with max_kv
+ * 131072 and total_kv 0 59 us, with total_kv known 30).  If they are
  * too small, a request's tokens from max_new on have no defined result, its own
  * keys from max_kv on are not seen, and with a total_kv that is too small the last
  * requests have no defined result.
@@ -664,8 +670,8 @@ hq_status hq_rope_kv(const hq_rope_desc* rope, const hq_kv_desc* kv, int32_t dty
  * bytes of the cache beyond the lengths are not read.  Pages outside the cache
  * read as zeros.  Rows at and past cu_new[B] are not written.  Products take
  * 16-bit operands (softmax weights rounded to dtype), sums are fp32, one rounding
- * at the end.  The order of the sums depends on shapes and lengths only, so
- * equal calls give equal bits.
+ * at the end.  The order of the sums depends on shapes, bounds and lengths only, so
+ * equal calls give equal bits.  out and lse must not overlap the inputs.
  */
 hq_status hq_attn_workspace_bytes(const hq_attn_desc* desc, const hq_kv_desc* kv, int64_t B, int64_t T,
                                   int64_t prefix_len, size_t* bytes);

@@ -22,11 +22,15 @@ def _build() -> str:
 
     os.makedirs(OUT, exist_ok=True)
     objs = []
+    sources = [*glob.glob(os.path.join(CSRC, "*")), os.path.join(ROOT, "include", "hq.h"), B.__file__, __file__]
+    newest = max(os.path.getmtime(f) for f in sources)
     for src in HOST:
         obj = os.path.join(OUT, "kv_" + src + ".o")
+        objs.append(obj)
+        if os.path.exists(obj) and os.path.getmtime(obj) > newest:
+            continue
         # (B.COMMON's -O3 stays for the kernels)
         _run([HIPCC, "-x", "hip", *B.COMMON, "-g", *_host_flags(), "-Xarch_host", "-O1", "-c", os.path.join(CSRC, src), "-o", obj])
-        objs.append(obj)
     for k in sorted(glob.glob(os.path.join(CSRC, "*.hip"))):
         if os.path.basename(k) not in HOST:
             obj = os.path.join(B.BUILD, os.path.basename(k) + ".o")
