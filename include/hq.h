@@ -670,7 +670,8 @@ hq_status hq_rope_kv(const hq_rope_desc* rope, const hq_kv_desc* kv, int32_t dty
  * bytes of the cache beyond the lengths are not read.  Pages outside the cache
  * read as zeros.  Rows at and past cu_new[B] are not written.  Products take
  * 16-bit operands (softmax weights rounded to dtype), sums are fp32, one rounding
- * at the end.  The order of the sums depends on shapes, bounds and lengths only, so
+ * at the end.  The sum of weights times values is divided last: bf16 values of
+ * which the number of keys times |v| passes 2^120 can overflow it.  The order of the sums depends on shapes, bounds and lengths only, so
  * equal calls give equal bits.  out and lse must not overlap the inputs.
  */
 hq_status hq_attn_workspace_bytes(const hq_attn_desc* desc, const hq_kv_desc* kv, int64_t B, int64_t T,
