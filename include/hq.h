@@ -581,10 +581,10 @@ typedef struct hq_rope_desc {
  * same result but for the order of its sums, and take longer: with total_kv 0,
  * every request is taken to be max_kv long, and workgroups get as many keys each
  * as that asks for (8 requests of 4000 keys, 32/8 heads of 128: 29 us; with max_kv
- * 131072 and total_kv 0 59 us, with total_kv known 30).  If they are
- * too small, a request's tokens from max_new on have no defined result, its own
- * keys from max_kv on are not seen, and with a total_kv that is too small the last
- * requests have no defined result.
+ * 131072 and total_kv 0 59 us, with total_kv known 30).  If they are too small, a
+ * request's tokens from max_new on have no defined result, its own keys from max_kv
+ * on are not seen, and with a total_kv that is too small the last requests have no
+ * defined result.
  */
 typedef struct hq_attn_desc {
     int32_t abi_version; /* HQ_ABI_VERSION                                 */
@@ -625,8 +625,9 @@ hq_status hq_kv_slots(int32_t block_size, int64_t B, int64_t T_cap, int64_t max_
 
 /*
  * Rotary table rows first_pos .. first_pos + count - 1: fp32 [count][rot_dim],
- * cos of the rot_dim/2 angles, then their sin.  Angles are reduced in 64 bits
- * from turns in two parts: right to 2^-30 of a turn at every position.  first_pos + count <= 2^31.
+ * cos of the rot_dim/2 angles, then their sin.  Angles are reduced in 64 bits from
+ * turns in two parts: right to 2^-30 of a turn at every position.
+ * first_pos + count <= 2^31.
  */
 hq_status hq_rope_table(const hq_rope_desc* rope, int64_t first_pos, int64_t count, float* table, hq_stream_t stream);
 
@@ -665,14 +666,15 @@ hq_status hq_rope_kv(const hq_rope_desc* rope, const hq_kv_desc* kv, int32_t dty
  *   k_scale, v_scale  fp32 [kv_heads] for an E4M3 cache, else NULL
  *   lse        fp32 [T][q_heads] or NULL: log sum_j exp(c(scale q.k_j))
  * A token that sees no key gets out = 0 and lse = -inf; one whose scores are all
- * -inf has no softmax and gets NaN.  Keys that a token does
- * not see never reach it, whatever they hold (NaN and infinities included);
- * bytes of the cache beyond the lengths are not read.  Pages outside the cache
- * read as zeros.  Rows at and past cu_new[B] are not written.  Products take
- * 16-bit operands (softmax weights rounded to dtype), sums are fp32, one rounding
- * at the end.  The sum of weights times values is divided last: bf16 values of
- * which the number of keys times |v| passes 2^120 can overflow it.  The order of the sums depends on shapes, bounds and lengths only, so
- * equal calls give equal bits.  out and lse must not overlap the inputs.
+ * -inf has no softmax and gets NaN.  Keys that a token does not see never reach it,
+ * whatever they hold (NaN and infinities included); bytes of the cache beyond the
+ * lengths are not read.  Pages outside the cache read as zeros.  Rows at and past
+ * cu_new[B] are not written.  Products take 16-bit operands (softmax weights rounded
+ * to dtype), sums are fp32, one rounding at the end.  The sum of weights times
+ * values is divided last: bf16 values of which the number of keys times |v| passes
+ * 2^120 can overflow it.  The order of the sums depends on shapes, bounds and
+ * lengths only, so equal calls give equal bits.  out and lse must not overlap the
+ * inputs.
  */
 hq_status hq_attn_workspace_bytes(const hq_attn_desc* desc, const hq_kv_desc* kv, int64_t B, int64_t T,
                                   int64_t prefix_len, size_t* bytes);
