@@ -18,6 +18,7 @@
 #include "hq_common.h"
 #include "hq_internal.h"
 #include "hq_kv.h"
+#include "hq_layer.h"
 
 namespace hq {
 
@@ -237,7 +238,8 @@ hq_status describe(const hq_layer_desc* d, LayerInfo* L) {
         I.G = 32;
     } else if (a == HQ_DT_FP8_E4M3 && w == HQ_DT_FP8_E4M3) {
         I.kind = Kind::FP8_BLOCK;
-        if (d->num_experts) return set_error(HQ_ERR_UNSUPPORTED, "blockwise FP8 is built for dense layers");
+        if (d->num_experts && pad16(d->N) * d->K >= (int64_t)1 << 31)
+            return set_error(HQ_ERR_UNSUPPORTED, "an FP8 expert's weights must stay below 2 GiB");
         if (d->a_scale != HQ_ASCALE_PER_BLOCK128_F32)
             return set_error(HQ_ERR_UNSUPPORTED, "FP8 W8A8 needs fp32 activation scales per 128-K block");
         if (d->w_scale_dtype != HQ_DT_FP32 || d->w_scale_gran != HQ_GRAN_BLOCK_128x128)
@@ -604,7 +606,8 @@ hq_status hq_workspace_bytes(const hq_layer_desc* desc, int64_t M_or_T, int32_t 
     if (M_or_T < 0 || M_or_T > (1LL << 30)) return set_error(HQ_ERR_INVALID_ARG, "M/T out of range");
     if (desc->num_experts) {
         if (top_k < 1 || top_k > desc->num_experts) return set_error(HQ_ERR_INVALID_ARG, "top_k out of range");
-        *bytes = moe_layout(M_or_T, top_k, desc->num_experts, true).bytes;  // Indexed needs the most
+        *bytes = L.kind == Kind::FP8_BLOCK ? moe_f8_workspace(M_or_T, top_k, desc->num_experts)
+                                           : moe_layout(M_or_T, top_k, desc->num_experts, true).bytes;  // Indexed needs the most
     } else {
         *bytes = dense_workspace(L, M_or_T);
     }
@@ -694,26 +697,54 @@ hq_status hq_moe_gemm(const hq_layer_desc* desc, int32_t mode, int64_t T, int32_
     LayerInfo L;
     hq_status st = describe(desc, &L);
     if (st != HQ_OK) return st;
-    if (!desc->num_experts || L.kind != Kind::MOE_MX_BF16)
+    if (!desc->num_experts || (L.kind != Kind::MOE_MX_BF16 && L.kind != Kind::FP8_BLOCK))
         return set_error(HQ_ERR_INVALID_ARG, "hq_moe_gemm takes a MoE descriptor (num_experts > 0)");
+    const bool f8 = L.kind == Kind::FP8_BLOCK;
     if (mode != HQ_MOE_INDEXED && mode != HQ_MOE_GROUPED) return set_error(HQ_ERR_INVALID_ARG, "bad MoE mode %d", mode);
     if (T < 0 || T > (1LL << 24)) return set_error(HQ_ERR_INVALID_ARG, "T=%lld out of range", (long long)T);
     if (top_k < 1 || top_k > desc->num_experts) return set_error(HQ_ERR_INVALID_ARG, "top_k=%d out of range", top_k);
     if (T == 0) return ok();
     const bool indexed = mode == HQ_MOE_INDEXED;
     if (!A || !w || !s || !D) return set_error(HQ_ERR_INVALID_ARG, "A, w, s and D are required");
-    if (a_scale || z || s2) return set_error(HQ_ERR_INVALID_ARG, "a_scale, z and s2 must be NULL for this format");
+    if ((a_scale != nullptr) != f8)
+        return set_error(HQ_ERR_INVALID_ARG, f8 ? "a_scale is required" : "a_scale must be NULL for this format");
+    if (z || s2) return set_error(HQ_ERR_INVALID_ARG, "z and s2 must be NULL for this format");
     if (indexed && (!topk_ids || expert_offsets))
         return set_error(HQ_ERR_INVALID_ARG, "INDEXED takes topk_ids and no expert_offsets");
     if (!indexed && (topk_ids || !expert_offsets))
         return set_error(HQ_ERR_INVALID_ARG, "GROUPED takes expert_offsets and no topk_ids");
     const int64_t P = T * top_k;
     const int64_t arows = indexed ? T : P;
-    if (arows * L.K * 2 >= (int64_t)1 << 32 || P * L.N >= (int64_t)1 << 31)
+    if (arows * L.K * (f8 ? 1 : 2) >= (int64_t)1 << 32 || P * L.N >= (int64_t)1 << 31)
         return set_error(HQ_ERR_UNSUPPORTED, "activation bytes must stay below 4 GiB and rows*N below 2^31");
     if (!aligned16(A) || !aligned16(w) || !aligned16(s) || !aligned16(D) || (topk_ids && !aligned16(topk_ids)) ||
-        (expert_offsets && !aligned16(expert_offsets)))
+        (expert_offsets && !aligned16(expert_offsets)) || (a_scale && !aligned16(a_scale)))
         return set_error(HQ_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+    if (f8) {
+        if ((desc->num_experts < P ? desc->num_experts : P) * cdiv(L.N, 128) >= (int64_t)1 << 23)
+            return set_error(HQ_ERR_UNSUPPORTED, "experts * N / 128 must stay below 2^23");
+        const size_t need = moe_f8_workspace(T, top_k, desc->num_experts);
+        if (!workspace || ws_bytes < need)
+            return set_error(HQ_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given", need, workspace ? ws_bytes : (size_t)0);
+        if (!aligned16(workspace)) return set_error(HQ_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+        MoeF8Args f{};
+        f.T = T;
+        f.N = L.N;
+        f.K = L.K;
+        f.top_k = top_k;
+        f.E = desc->num_experts;
+        f.indexed = indexed;
+        f.A = A;
+        f.sa = a_scale;
+        f.ids = topk_ids;
+        f.offsets = expert_offsets;
+        f.w = w;
+        f.s = s;
+        f.D = D;
+        f.ws = workspace;
+        f.stream = (hipStream_t)stream;
+        return hip_status(moe_f8_launch(f), indexed ? "hq_moe_gemm(FP8 INDEXED)" : "hq_moe_gemm(FP8 GROUPED)");
+    }
     const MoeLayout lay = moe_layout(T, top_k, desc->num_experts, indexed);
     if (!workspace || ws_bytes < lay.bytes)
         return set_error(HQ_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given", lay.bytes,
@@ -791,6 +822,159 @@ hq_status hq_silu_mul(int32_t dtype, int64_t rows, int64_t I, const void* gate_u
     if (!gate_up || !out) return set_error(HQ_ERR_INVALID_ARG, "gate_up and out are required");
     if (!aligned16(gate_up) || !aligned16(out)) return set_error(HQ_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
     return hip_status(silu_mul_launch(rows, I, gate_up, out, (hipStream_t)stream), "hq_silu_mul");
+}
+
+static hq_status row_out(int32_t dtype, int32_t out_dtype, int32_t a_scale, int64_t width, RowOut* out) {
+    if (a_scale == HQ_ASCALE_NONE && out_dtype == dtype) *out = RowOut::SAME16;
+    else if (a_scale == HQ_ASCALE_PER_TOKEN_F32 && out_dtype == HQ_DT_FP8_E4M3) *out = RowOut::TOKEN_F8;
+    else if (a_scale == HQ_ASCALE_PER_TOKEN_F32 && out_dtype == HQ_DT_INT8) *out = RowOut::TOKEN_I8;
+    else if (a_scale == HQ_ASCALE_PER_BLOCK128_F32 && out_dtype == HQ_DT_FP8_E4M3) *out = RowOut::BLOCK_F8;
+    else if (a_scale == HQ_ASCALE_MX_E8M0 && out_dtype == HQ_DT_FP8_E4M3) *out = RowOut::MX_F8;
+    else if (a_scale == HQ_ASCALE_MX_E8M0 && out_dtype == HQ_DT_FP4_E2M1) *out = RowOut::MX_F4;
+    else return set_error(HQ_ERR_UNSUPPORTED, "no output of dtype %d with scales %d", out_dtype, a_scale);
+    const int64_t whole = *out == RowOut::BLOCK_F8 ? 128 : *out == RowOut::MX_F8 || *out == RowOut::MX_F4 ? 32 : 1;
+    if (width % whole) return set_error(HQ_ERR_UNSUPPORTED, "these scales need rows of a multiple of %lld", (long long)whole);
+    return HQ_OK;
+}
+
+hq_status hq_rmsnorm(const hq_norm_desc* d, int64_t M, int64_t K, const void* x, int64_t x_stride, const void* residual,
+                     int64_t residual_stride, const void* weight, void* sum_out, int64_t sum_stride, void* out,
+                     void* out_scale, hq_stream_t stream) {
+    if (!d) return set_error(HQ_ERR_INVALID_ARG, "norm descriptor is NULL");
+    if (d->abi_version != HQ_ABI_VERSION) return set_error(HQ_ERR_ABI, "norm abi_version %d, library has %d", d->abi_version, HQ_ABI_VERSION);
+    if (d->reserved) return set_error(HQ_ERR_INVALID_ARG, "norm reserved field must be zero");
+    if (d->dtype != HQ_DT_BF16 && d->dtype != HQ_DT_FP16) return set_error(HQ_ERR_UNSUPPORTED, "norm dtype %d (BF16 or FP16)", d->dtype);
+    if (d->weight_dtype != d->dtype && d->weight_dtype != HQ_DT_FP32)
+        return set_error(HQ_ERR_UNSUPPORTED, "norm weight dtype %d (that of x, or FP32)", d->weight_dtype);
+    if (!(d->eps >= 0.f) || !std::isfinite(d->eps) || !std::isfinite(d->weight_offset))
+        return set_error(HQ_ERR_INVALID_ARG, "eps must be 0 or positive, weight_offset finite");
+    if (M < 0 || M > (1LL << 22) || K < 1) return set_error(HQ_ERR_INVALID_ARG, "M=%lld K=%lld out of range", (long long)M, (long long)K);
+    if (K > kRowMaxWidth) return set_error(HQ_ERR_UNSUPPORTED, "rows of at most %d elements are built", kRowMaxWidth);
+    RowArgs a{};
+    const hq_status st = row_out(d->dtype, d->out_dtype, d->a_scale, K, &a.kind);
+    if (st != HQ_OK) return st;
+    const int64_t most = (int64_t)1 << 31;
+    if (x_stride < K || x_stride >= most || (residual && (residual_stride < K || residual_stride >= most)) ||
+        (sum_out && (sum_stride < K || sum_stride >= most)))
+        return set_error(HQ_ERR_INVALID_ARG, "row strides must be at least K, below 2^31");
+    if (K % 32 == 0 && a.kind != RowOut::SAME16 && d->a_scale != HQ_ASCALE_PER_TOKEN_F32 &&
+        (x_stride % 8 || (residual && residual_stride % 8) || (sum_out && sum_stride % 8)))
+        return set_error(HQ_ERR_UNSUPPORTED, "block scales need row strides that are multiples of 8");
+    if (M == 0) return ok();
+    if (!x || !weight || !out) return set_error(HQ_ERR_INVALID_ARG, "x, weight and out are required");
+    if ((out_scale != nullptr) != (a.kind != RowOut::SAME16))
+        return set_error(HQ_ERR_INVALID_ARG, out_scale ? "out_scale must be NULL for a 16-bit output" : "out_scale is required");
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(sum_out) || !aligned16(out) || !aligned16(out_scale))
+        return set_error(HQ_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+    a.bf16 = d->dtype == HQ_DT_BF16;
+    a.w_f32 = d->weight_dtype == HQ_DT_FP32;
+    a.rows = M;
+    a.width = (int)K;
+    a.eps = d->eps;
+    a.w_offset = d->weight_offset;
+    a.x = x;
+    a.res = residual;
+    a.w = weight;
+    a.x_stride = x_stride;
+    a.res_stride = residual_stride;
+    a.sum_stride = sum_stride;
+    a.sum = sum_out;
+    a.out = out;
+    a.scale = out_scale;
+    a.stream = (hipStream_t)stream;
+    return hip_status(row_launch(a), "hq_rmsnorm");
+}
+
+hq_status hq_silu_mul_quant(int32_t dtype, int32_t out_dtype, int32_t a_scale, int64_t rows, int64_t I, const void* gate_up, void* out,
+                            void* out_scale, hq_stream_t stream) {
+    if (dtype != HQ_DT_BF16 && dtype != HQ_DT_FP16) return set_error(HQ_ERR_UNSUPPORTED, "dtype %d (BF16 or FP16)", dtype);
+    if (rows < 0 || rows > (1LL << 22) || I < 8 || I % 8)
+        return set_error(HQ_ERR_INVALID_ARG, "rows=%lld I=%lld out of range (I a multiple of 8)", (long long)rows, (long long)I);
+    if (I > kRowMaxWidth) return set_error(HQ_ERR_UNSUPPORTED, "rows of at most %d elements are built", kRowMaxWidth);
+    RowArgs a{};
+    const hq_status st = row_out(dtype, out_dtype, a_scale, I, &a.kind);
+    if (st != HQ_OK) return st;
+    if (a.kind == RowOut::SAME16) return set_error(HQ_ERR_UNSUPPORTED, "the output is quantised (16 bits: hq_silu_mul)");
+    if (rows == 0) return ok();
+    if (!gate_up || !out || !out_scale) return set_error(HQ_ERR_INVALID_ARG, "gate_up, out and out_scale are required");
+    if (!aligned16(gate_up) || !aligned16(out) || !aligned16(out_scale)) return set_error(HQ_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+    a.silu = true;
+    a.bf16 = dtype == HQ_DT_BF16;
+    a.rows = rows;
+    a.width = (int)I;
+    a.x = gate_up;
+    a.x_stride = 2 * I;
+    a.out = out;
+    a.scale = out_scale;
+    a.stream = (hipStream_t)stream;
+    return hip_status(row_launch(a), "hq_silu_mul_quant");
+}
+
+hq_status hq_moe_route(const hq_route_desc* d, int64_t T, const void* logits, int64_t logits_stride, const float* bias, int32_t* topk_ids,
+                       float* topk_weights, hq_stream_t stream) {
+    if (!d) return set_error(HQ_ERR_INVALID_ARG, "route descriptor is NULL");
+    if (d->abi_version != HQ_ABI_VERSION) return set_error(HQ_ERR_ABI, "route abi_version %d, library has %d", d->abi_version, HQ_ABI_VERSION);
+    if (d->reserved) return set_error(HQ_ERR_INVALID_ARG, "route reserved field must be zero");
+    if (d->dtype != HQ_DT_FP32 && d->dtype != HQ_DT_BF16 && d->dtype != HQ_DT_FP16)
+        return set_error(HQ_ERR_UNSUPPORTED, "logits dtype %d (FP32, BF16 or FP16)", d->dtype);
+    if (d->scoring != HQ_ROUTE_SOFTMAX && d->scoring != HQ_ROUTE_SIGMOID) return set_error(HQ_ERR_INVALID_ARG, "bad scoring %d", d->scoring);
+    if (d->renormalize != 0 && d->renormalize != 1) return set_error(HQ_ERR_INVALID_ARG, "renormalize is 0 or 1");
+    if (!std::isfinite(d->scale)) return set_error(HQ_ERR_INVALID_ARG, "scale must be finite");
+    if (d->num_experts < 1 || d->num_experts > kRouteMaxExperts) return set_error(HQ_ERR_INVALID_ARG, "num_experts=%d out of range [1, %d]", d->num_experts, kRouteMaxExperts);
+    if (d->groups < 1 || d->groups > kRouteMaxGroups || d->num_experts % d->groups)
+        return set_error(HQ_ERR_INVALID_ARG, "groups=%d: 1..%d, dividing num_experts", d->groups, kRouteMaxGroups);
+    const int members = d->num_experts / d->groups;
+    if (d->top_groups < 1 || d->top_groups > d->groups) return set_error(HQ_ERR_INVALID_ARG, "top_groups=%d out of range", d->top_groups);
+    if (d->group_best < 1 || d->group_best > 2 || (d->groups > 1 && d->group_best > members))
+        return set_error(HQ_ERR_INVALID_ARG, "group_best is 1 or 2, at most a group's experts");
+    if (d->top_k < 1 || d->top_k > kRouteMaxTopK || d->top_k > members * d->top_groups)
+        return set_error(HQ_ERR_INVALID_ARG, "top_k=%d: 1..%d, at most the experts of top_groups groups", d->top_k, kRouteMaxTopK);
+    if (T < 0 || T > (1LL << 24)) return set_error(HQ_ERR_INVALID_ARG, "T=%lld out of range", (long long)T);
+    if (logits_stride < d->num_experts || logits_stride >= (int64_t)1 << 31)
+        return set_error(HQ_ERR_INVALID_ARG, "logits_stride must be at least num_experts, below 2^31");
+    if (T == 0) return ok();
+    if (!logits || !topk_ids || !topk_weights) return set_error(HQ_ERR_INVALID_ARG, "logits, topk_ids and topk_weights are required");
+    if (!aligned16(logits) || !aligned16(bias) || !aligned16(topk_ids) || !aligned16(topk_weights))
+        return set_error(HQ_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+    RouteArgs a{};
+    a.dtype = d->dtype;
+    a.experts = d->num_experts;
+    a.top_k = d->top_k;
+    a.groups = d->groups;
+    a.top_groups = d->top_groups;
+    a.group_best = d->group_best;
+    a.sigmoid = d->scoring == HQ_ROUTE_SIGMOID;
+    a.renorm = d->renormalize != 0;
+    a.scale = d->scale;
+    a.T = T;
+    a.stride = logits_stride;
+    a.logits = logits;
+    a.bias = bias;
+    a.ids = topk_ids;
+    a.weights = topk_weights;
+    a.stream = (hipStream_t)stream;
+    return hip_status(route_launch(a), "hq_moe_route");
+}
+
+hq_status hq_moe_combine(int32_t dtype, int64_t T, int32_t top_k, int64_t N, const void* y, const float* topk_weights,
+                         const int32_t* sorted_pairs, const void* add, void* out, void* workspace, size_t ws_bytes,
+                         hq_stream_t stream) {
+    if (dtype != HQ_DT_BF16 && dtype != HQ_DT_FP16) return set_error(HQ_ERR_UNSUPPORTED, "dtype %d (BF16 or FP16)", dtype);
+    if (T < 0 || T > (1LL << 23) || top_k < 1 || top_k > 4096 || N < 1 || N > (1LL << 21))
+        return set_error(HQ_ERR_INVALID_ARG, "T, top_k or N out of range");
+    if (T * top_k >= (1LL << 31)) return set_error(HQ_ERR_UNSUPPORTED, "T*top_k must stay below 2^31");
+    if (T == 0) return ok();
+    if (!y || !topk_weights || !out) return set_error(HQ_ERR_INVALID_ARG, "y, topk_weights and out are required");
+    if (!aligned16(y) || !aligned16(topk_weights) || !aligned16(sorted_pairs) || !aligned16(add) || !aligned16(out))
+        return set_error(HQ_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+    if (sorted_pairs) {
+        const size_t need = (size_t)(T * top_k) * 4;
+        if (!workspace || ws_bytes < need)
+            return set_error(HQ_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given", need, workspace ? ws_bytes : (size_t)0);
+        if (!aligned16(workspace)) return set_error(HQ_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+    }
+    CombineArgs a{dtype == HQ_DT_BF16, T, N, top_k, y, add, topk_weights, sorted_pairs, out, (int32_t*)workspace, (hipStream_t)stream};
+    return hip_status(combine_launch(a), "hq_moe_combine");
 }
 
 hq_status hq_kv_slots(int32_t block_size, int64_t B, int64_t T_cap, int64_t max_blocks, int64_t first_pos,
@@ -1036,16 +1220,19 @@ hq_status hq_moe_gather(int32_t dtype, int64_t T, int32_t top_k, int64_t K, cons
         case HQ_DT_FP16: eb = 2; break;
         case HQ_DT_FP8_E4M3:
         case HQ_DT_INT8: eb = 1; break;
-        default: return set_error(HQ_ERR_UNSUPPORTED, "gather dtype must be BF16, FP16, FP8_E4M3 or INT8");
+        case HQ_DT_FP32: eb = 4; break;
+        default: return set_error(HQ_ERR_UNSUPPORTED, "gather dtype must be BF16, FP16, FP8_E4M3, INT8 or FP32");
     }
     if (T < 0 || top_k < 1 || K < 1 || T > (1LL << 24) || K > (1LL << 24) || top_k > 4096)
         return set_error(HQ_ERR_INVALID_ARG, "sizes out of range");
     if (T * top_k >= (1LL << 31)) return set_error(HQ_ERR_UNSUPPORTED, "T*top_k must stay below 2^31");
     if (T == 0) return ok();
-    if ((K * eb) % 16) return set_error(HQ_ERR_UNSUPPORTED, "row bytes must be a multiple of 16");
+    if ((K * eb) % 16 && dtype != HQ_DT_FP32) return set_error(HQ_ERR_UNSUPPORTED, "row bytes must be a multiple of 16");
     if (!A || !sorted_pairs || !A_sorted) return set_error(HQ_ERR_INVALID_ARG, "pointers are required");
     if (!aligned16(A) || !aligned16(sorted_pairs) || !aligned16(A_sorted))
         return set_error(HQ_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+    if ((K * eb) % 16)
+        return hip_status(gather_words_launch(A, sorted_pairs, T * top_k, top_k, K, A_sorted, (hipStream_t)stream), "hq_moe_gather");
     return hip_status(moe_gather_launch(A, sorted_pairs, T * top_k, top_k, K * eb, A_sorted, (hipStream_t)stream),
                       "hq_moe_gather");
 }

@@ -1,0 +1,349 @@
+// Rows that become the next product's activations: RMS norm (with the
+// residual's addition) and SwiGLU, each with a 16-bit or a quantised output.
+//
+//   norm:    h = x + r,  y = h (mean h^2 + eps)^-1/2 (w + offset)
+//   SwiGLU:  y = silu(gate) up,  silu(g) = g / (1 + e^-g)
+//   tokens:  s = max|y| / top over the row (top: E4M3 448, INT8 127; 1 for zeros), q = rnd(y / s)
+//   blocks:  the same over 128 consecutive elements (E4M3)
+//   MX:      E8M0 per 32: the exponent of max|y| less emax (E4M3 8, E2M1 2), q = rnd(y 2^(127 - e))
+//
+// All of it is bound by HBM: each element is read once and its code written
+// once.  A row stays in registers, 8 consecutive elements a group, so the sum of
+// squares, the maximum and the rounding need no second pass over memory; y is
+// formed in fp32 from the unrounded h and rounded once.
+#include "hq_device.hpp"
+#include "hq_layer.h"
+
+namespace hq {
+
+namespace {
+
+struct RowParams {
+    const void *x, *res, *w;
+    void *sum, *out, *scale;
+    int64_t rows, x_stride, res_stride, sum_stride;
+    int width;
+    float eps, w_offset;
+    int silu, w_f32, fp4_or_i8;
+};
+
+enum class Quant { SAME16, TOKEN, BLOCK, MX };
+
+__device__ __forceinline__ float amax8(const float (&y)[8]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
+    return m;
+}
+
+// Four E4M3 codes: rounded to nearest even, saturated at +-448, NaN kept (0x7F).
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    auto sat = [](float v) { return fminf(fmaxf(v, -448.f), 448.f); };
+    int pk = __builtin_amdgcn_cvt_pk_fp8_f32(sat(a), sat(b), 0, false);
+    pk = __builtin_amdgcn_cvt_pk_fp8_f32(sat(c), sat(d), pk, true);
+    uint32_t u = (uint32_t)pk;
+    auto nan_fix = [&](int byte, float v) { u = v != v ? (u & ~(0xFFu << (8 * byte))) | (0x7Fu << (8 * byte)) : u; };
+    nan_fix(0, a);
+    nan_fix(1, b);
+    nan_fix(2, c);
+    nan_fix(3, d);
+    return u;
+}
+
+// INT8 in -127..127, to nearest even; NaN becomes 0.
+__device__ __forceinline__ uint32_t int8_code(float v) {
+    return (uint32_t)(v != v ? 0 : (int)rintf(fminf(fmaxf(v, -127.f), 127.f))) & 0xFFu;
+}
+
+// E2M1 code of v with the sign of x: a midpoint of the grid 0, .5, 1, 1.5, 2, 3, 4, 6
+// goes to the neighbour with the even mantissa bit.
+__device__ __forceinline__ uint32_t e2m1_of(float x, float v) {
+    const float a = fabsf(v);
+    const uint32_t mag = (uint32_t)(a > 0.25f) + (uint32_t)(a >= 0.75f) + (uint32_t)(a > 1.25f) + (uint32_t)(a >= 1.75f) +
+                         (uint32_t)(a > 2.5f) + (uint32_t)(a >= 3.5f) + (uint32_t)(a > 5.0f);
+    return mag | ((__float_as_uint(x) >> 28) & 8u);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(v4u v, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t u = v[i];
+        f[2 * i] = bits16_to_f32<BF16>((uint16_t)u);
+        f[2 * i + 1] = bits16_to_f32<BF16>((uint16_t)(u >> 16));
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ v4u pack8(const float (&f)[8]) {
+    v4u v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (uint32_t)f32_to_16<BF16>(f[2 * i]) | ((uint32_t)f32_to_16<BF16>(f[2 * i + 1]) << 16);
+    return v;
+}
+
+// Sum or maximum over the TPR threads of a row (TPR 64: one wave; else the whole workgroup).
+template <int TPR, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* red) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        const float o = __shfl_xor(v, off);
+        v = MAX ? fmaxf(v, o) : v + o;
+    }
+    if constexpr (TPR > 64) {
+        constexpr int NW = TPR / 64;
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) v = MAX ? fmaxf(v, red[i]) : v + red[i];
+    }
+    return v;
+}
+
+// TPR threads hold a row of at most 8 NV TPR elements.  VEC: 16-byte loads, thread
+// i holding the groups i, i + TPR, ... (so a block of 128 is 16 neighbouring lanes
+// and one of 32 is 4).  Without it (rows or strides that are not multiples of 8)
+// the elements i, i + TPR, ...: 2-byte loads that are consecutive over a wave; no
+// block scales.
+template <bool BF16, Quant Q, int TPR, int NV, bool VEC>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(RowParams p) {
+    static_assert(VEC || Q == Quant::SAME16 || Q == Quant::TOKEN, "block scales need whole groups");
+    __shared__ float red[2][16];
+    constexpr int RPW = TPR < 256 ? 256 / TPR : 1;  // rows per workgroup
+    const int t = threadIdx.x % TPR;
+    const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
+    if (RPW > 1 && row >= p.rows) return;  // (whole waves; no barrier below where RPW > 1)
+    const int K = p.width;
+    auto el = [&](int j, int u) { return VEC ? (j * TPR + t) * 8 + u : (j * 8 + u) * TPR + t; };
+
+    float y[NV][8];
+    float ss = 0.f;
+    if (p.silu) {
+        const uint16_t* in = (const uint16_t*)p.x + row * p.x_stride;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float g[8], u[8];
+            const bool live = el(j, 0) < K;
+            unpack8<BF16>(live ? ld16(in + el(j, 0)) : v4u{0, 0, 0, 0}, g);
+            unpack8<BF16>(live ? ld16(in + K + el(j, 0)) : v4u{0, 0, 0, 0}, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // e^-|g| <= 1: no overflow at either end
+                const float e = expf(-fabsf(g[i]));
+                y[j][i] = (g[i] >= 0.f ? g[i] : g[i] * e) / (1.0f + e) * u[i];
+            }
+        }
+    } else {
+        const uint16_t* x = (const uint16_t*)p.x + row * p.x_stride;
+        const uint16_t* r = p.res ? (const uint16_t*)p.res + row * p.res_stride : nullptr;
+        uint16_t* sum = p.sum ? (uint16_t*)p.sum + row * p.sum_stride : nullptr;
+        if constexpr (VEC) {
+            v4u xv[NV], rv[NV];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) xv[j] = el(j, 0) < K ? ld16(x + el(j, 0)) : v4u{0, 0, 0, 0};
+            if (r) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) rv[j] = el(j, 0) < K ? ld16(r + el(j, 0)) : v4u{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                unpack8<BF16>(xv[j], y[j]);
+                if (r) {
+                    float a[8];
+                    unpack8<BF16>(rv[j], a);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[j][i] += a[i];
+                }
+                if (sum && el(j, 0) < K) *(v4u*)(sum + el(j, 0)) = pack8<BF16>(y[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss += y[j][i] * y[j][i];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[j][i] = el(j, i) < K ? bits16_to_f32<BF16>(x[el(j, i)]) : 0.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (r && el(j, i) < K) y[j][i] += bits16_to_f32<BF16>(r[el(j, i)]);
+                    if (sum && el(j, i) < K) sum[el(j, i)] = f32_to_16<BF16>(y[j][i]);
+                    ss += y[j][i] * y[j][i];
+                }
+        }
+        ss = row_reduce<TPR, false>(ss, red[0]);
+        const float rs = 1.0f / sqrtf(ss / (float)K + p.eps);
+        const uint16_t* w16 = (const uint16_t*)p.w;
+        const float* w32 = (const float*)p.w;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float w[8];
+            if constexpr (VEC) {
+                if (el(j, 0) >= K) continue;  // zeros stay
+                if (p.w_f32) {
+                    *(v4f*)&w[0] = *(const v4f*)(w32 + el(j, 0));
+                    *(v4f*)&w[4] = *(const v4f*)(w32 + el(j, 0) + 4);
+                } else {
+                    unpack8<BF16>(ld16(w16 + el(j, 0)), w);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = el(j, i) >= K ? 0.f : p.w_f32 ? w32[el(j, i)] : bits16_to_f32<BF16>(w16[el(j, i)]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (VEC || el(j, i) < K) y[j][i] = y[j][i] * rs * (w[i] + p.w_offset);
+        }
+    }
+
+    if constexpr (Q == Quant::SAME16) {
+        uint16_t* out = (uint16_t*)p.out + row * K;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if constexpr (VEC) {
+                if (el(j, 0) < K) *(v4u*)(out + el(j, 0)) = pack8<BF16>(y[j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (el(j, i) < K) out[el(j, i)] = f32_to_16<BF16>(y[j][i]);
+            }
+        }
+    } else if constexpr (Q == Quant::MX) {
+        // the 4 lanes of a block of 32 share an exponent; a block that holds a NaN or
+        // an infinity has E8M0 255 and zero codes
+        const bool fp4 = p.fp4_or_i8 != 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float m = amax8(y[j]);
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) bad |= (uint32_t)((__float_as_uint(y[j][i]) & 0x7F800000u) == 0x7F800000u);
+            m = fmaxf(m, __shfl_xor(m, 1));
+            m = fmaxf(m, __shfl_xor(m, 2));
+            bad |= __shfl_xor(bad, 1);
+            bad |= __shfl_xor(bad, 2);
+            int e = 0;
+            if (bad) {
+                e = 255;
+            } else if (m > 0.f) {
+                e = (int)((__float_as_uint(m) >> 23) & 0xFFu) - (fp4 ? 2 : 8);
+                e = e < 0 ? 0 : e;
+            }
+            if (el(j, 0) >= K) continue;
+            const int64_t at = row * K + el(j, 0);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = e == 255 ? 0.f : ldexpf(y[j][i], 127 - e);
+            if (fp4) {
+                uint32_t q = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q |= (e == 255 ? 0u : e2m1_of(y[j][i], v[i])) << (4 * i);
+                *(uint32_t*)((char*)p.out + at / 2) = q;
+            } else {
+                *(uint2*)((char*)p.out + at) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+            }
+            if ((t & 3) == 0) ((uint8_t*)p.scale)[at / 32] = (uint8_t)e;
+        }
+    } else {
+        const bool i8 = Q == Quant::TOKEN && p.fp4_or_i8 != 0;
+        const float top = i8 ? 127.f : 448.f;
+        float s = 1.f;
+        if constexpr (Q == Quant::TOKEN) {
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) m = fmaxf(m, amax8(y[j]));
+            m = row_reduce<TPR, true>(m, red[1]);
+            s = m > 0.f ? m / top : 1.f;
+            if (t == 0) ((float*)p.scale)[row] = s;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if constexpr (Q == Quant::BLOCK) {
+                float m = amax8(y[j]);
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+                s = m > 0.f ? m / top : 1.f;
+                if ((t & 15) == 0 && el(j, 0) < K) ((float*)p.scale)[row * (K / 128) + el(j, 0) / 128] = s;
+            }
+            if constexpr (VEC) {
+                if (el(j, 0) >= K) continue;
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = y[j][i] / s;
+                uint2 q;
+                if (i8) {
+                    q.x = int8_code(v[0]) | int8_code(v[1]) << 8 | int8_code(v[2]) << 16 | int8_code(v[3]) << 24;
+                    q.y = int8_code(v[4]) | int8_code(v[5]) << 8 | int8_code(v[6]) << 16 | int8_code(v[7]) << 24;
+                } else {
+                    q = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+                }
+                *(uint2*)((char*)p.out + row * K + el(j, 0)) = q;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (el(j, i) < K) {
+                        const float v = y[j][i] / s;
+                        ((uint8_t*)p.out)[row * K + el(j, i)] = (uint8_t)(i8 ? int8_code(v) : e4m3x4(v, 0.f, 0.f, 0.f) & 0xFFu);
+                    }
+            }
+        }
+    }
+}
+
+template <bool BF16, Quant Q, int TPR, int NV, bool VEC>
+hipError_t go(const RowParams& p, hipStream_t st) {
+    constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
+    hipLaunchKernelGGL((row_kernel<BF16, Q, TPR, NV, VEC>), dim3((unsigned)((p.rows + RPW - 1) / RPW)), dim3(TPR < 256 ? 256 : TPR), 0, st, p);
+    return hipGetLastError();
+}
+
+template <bool BF16, Quant Q>
+hipError_t pick(const RowParams& p, bool vec, hipStream_t st) {
+    const int K = p.width;
+    if constexpr (Q == Quant::SAME16 || Q == Quant::TOKEN) {
+        if (!vec) {
+            if (K <= 4096) return go<BF16, Q, 256, 2, false>(p, st);
+            if (K <= 16384) return go<BF16, Q, 1024, 2, false>(p, st);
+            return go<BF16, Q, 1024, 8, false>(p, st);
+        }
+    }
+    if (K <= 512) return go<BF16, Q, 64, 1, true>(p, st);
+    if (K <= 2048) return go<BF16, Q, 256, 1, true>(p, st);
+    if (K <= 4096) return go<BF16, Q, 256, 2, true>(p, st);
+    if (K <= 8192) return go<BF16, Q, 256, 4, true>(p, st);
+    if (K <= 16384) return go<BF16, Q, 1024, 2, true>(p, st);
+    return go<BF16, Q, 1024, 8, true>(p, st);
+}
+
+}  // namespace
+
+hipError_t row_launch(const RowArgs& a) {
+    RowParams p{};
+    p.x = a.x;
+    p.res = a.res;
+    p.w = a.w;
+    p.sum = a.sum;
+    p.out = a.out;
+    p.scale = a.scale;
+    p.rows = a.rows;
+    p.x_stride = a.x_stride;
+    p.res_stride = a.res_stride;
+    p.sum_stride = a.sum_stride;
+    p.width = a.width;
+    p.eps = a.eps;
+    p.w_offset = a.w_offset;
+    p.silu = a.silu;
+    p.w_f32 = a.w_f32;
+    p.fp4_or_i8 = a.kind == RowOut::TOKEN_I8 || a.kind == RowOut::MX_F4;
+    const bool vec = a.width % 8 == 0 && a.x_stride % 8 == 0 && (!a.res || a.res_stride % 8 == 0) && (!a.sum || a.sum_stride % 8 == 0);
+    switch (a.kind) {
+        case RowOut::SAME16: return a.bf16 ? pick<true, Quant::SAME16>(p, vec, a.stream) : pick<false, Quant::SAME16>(p, vec, a.stream);
+        case RowOut::TOKEN_F8:
+        case RowOut::TOKEN_I8: return a.bf16 ? pick<true, Quant::TOKEN>(p, vec, a.stream) : pick<false, Quant::TOKEN>(p, vec, a.stream);
+        case RowOut::BLOCK_F8: return a.bf16 ? pick<true, Quant::BLOCK>(p, vec, a.stream) : pick<false, Quant::BLOCK>(p, vec, a.stream);
+        default: return a.bf16 ? pick<true, Quant::MX>(p, vec, a.stream) : pick<false, Quant::MX>(p, vec, a.stream);
+    }
+}
+
+}  // namespace hq

@@ -34,6 +34,7 @@ HQ_FLAG_BATCH_INVARIANT = 1
 HQ_ROPE_HALF, HQ_ROPE_INTERLEAVED = 1, 2
 HQ_ROPE_NONE, HQ_ROPE_LINEAR, HQ_ROPE_NTK, HQ_ROPE_PARTS = range(4)
 HQ_KV_MAX_REQUESTS = 4096
+HQ_ROUTE_SOFTMAX, HQ_ROUTE_SIGMOID = 1, 2
 HQ_TUNE_STREAM, HQ_TUNE_T128, HQ_TUNE_T256, HQ_TUNE_W128, HQ_TUNE_W256, HQ_TUNE_STREAM8 = 1, 2, 3, 4, 5, 6
 
 
@@ -81,6 +82,21 @@ class hq_attn_desc(C.Structure):
     ]
 
 
+class hq_norm_desc(C.Structure):
+    _fields_ = [
+        ("abi_version", C.c_int32), ("dtype", C.c_int32), ("weight_dtype", C.c_int32), ("out_dtype", C.c_int32),
+        ("a_scale", C.c_int32), ("eps", C.c_float), ("weight_offset", C.c_float), ("reserved", C.c_int32),
+    ]
+
+
+class hq_route_desc(C.Structure):
+    _fields_ = [
+        ("abi_version", C.c_int32), ("dtype", C.c_int32), ("num_experts", C.c_int32), ("top_k", C.c_int32),
+        ("scoring", C.c_int32), ("renormalize", C.c_int32), ("groups", C.c_int32), ("top_groups", C.c_int32),
+        ("group_best", C.c_int32), ("scale", C.c_float), ("reserved", C.c_int32),
+    ]
+
+
 _lib = None
 
 _P = C.c_void_p
@@ -104,6 +120,10 @@ _SIGS = {
     "hq_moe_align": (C.c_int, [C.c_int64, C.c_int32, C.c_int32, _P, _P, _P, _P, C.c_size_t, _P]),
     "hq_moe_gather": (C.c_int, [C.c_int32, C.c_int64, C.c_int32, C.c_int64, _P, _P, _P, _P]),
     "hq_silu_mul": (C.c_int, [C.c_int32, C.c_int64, C.c_int64, _P, _P, _P]),
+    "hq_rmsnorm": (C.c_int, [_P, C.c_int64, C.c_int64, _P, C.c_int64, _P, C.c_int64, _P, _P, C.c_int64, _P, _P, _P]),
+    "hq_silu_mul_quant": (C.c_int, [C.c_int32, C.c_int32, C.c_int32, C.c_int64, C.c_int64, _P, _P, _P, _P]),
+    "hq_moe_route": (C.c_int, [_P, C.c_int64, _P, C.c_int64, _P, _P, _P, _P]),
+    "hq_moe_combine": (C.c_int, [C.c_int32, C.c_int64, C.c_int32, C.c_int64, _P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
     "hq_kv_slots": (C.c_int, [C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_int64, _P, _P, _P, C.c_int64, _P, _P, _P, _P,
                               _P, _P, _P]),
     "hq_rope_table": (C.c_int, [_P, C.c_int64, C.c_int64, _P, _P]),
@@ -298,6 +318,29 @@ def desc_moe_mxfp4(E, N, K) -> hq_layer_desc:
                      num_experts=E)
 
 
+def desc_moe_fp8_blockwise(E, N, K) -> hq_layer_desc:
+    """Experts in FP8 with blockwise scales: each expert a layer of desc_fp8_blockwise."""
+    d = desc_fp8_blockwise(N, K)
+    d.num_experts = E
+    return d
+
+
+def norm_desc(dtype, out_dtype, a_scale=HQ_ASCALE_NONE, eps=1e-6, weight_dtype=None, weight_offset=0.0) -> hq_norm_desc:
+    d = hq_norm_desc()
+    d.abi_version, d.dtype, d.weight_dtype = HQ_ABI_VERSION, dtype, dtype if weight_dtype is None else weight_dtype
+    d.out_dtype, d.a_scale, d.eps, d.weight_offset = out_dtype, a_scale, eps, weight_offset
+    return d
+
+
+def route_desc(dtype, num_experts, top_k, sigmoid=False, renormalize=True, groups=1, top_groups=1, group_best=1,
+               scale=1.0) -> hq_route_desc:
+    d = hq_route_desc()
+    d.abi_version, d.dtype, d.num_experts, d.top_k = HQ_ABI_VERSION, dtype, num_experts, top_k
+    d.scoring, d.renormalize = HQ_ROUTE_SIGMOID if sigmoid else HQ_ROUTE_SOFTMAX, int(renormalize)
+    d.groups, d.top_groups, d.group_best, d.scale = groups, top_groups, group_best, scale
+    return d
+
+
 def kv_desc(dtype, num_blocks, block_size, kv_heads, head_dim, head_major=False) -> hq_kv_desc:
     """A dense paged cache: pages of [token][head][element], or [head][token][element] (head_major)."""
     d = hq_kv_desc()
@@ -437,6 +480,28 @@ def hq_probe_mfma(dtype, workgroups, iters, sink, stream=None) -> float:
 
 def hq_silu_mul(dtype, rows, I, gate_up, out, stream=None) -> None:
     _check(lib().hq_silu_mul(dtype, rows, I, _dp(gate_up), _dp(out), _stream(stream)), "hq_silu_mul")
+
+
+def hq_rmsnorm(desc, M, K, x, x_stride, weight, out, out_scale=None, residual=None, residual_stride=0, sum_out=None, sum_stride=0,
+               stream=None) -> None:
+    _check(lib().hq_rmsnorm(C.byref(desc), M, K, _dp(x), x_stride, _dp(residual), residual_stride, _dp(weight), _dp(sum_out),
+                            sum_stride, _dp(out), _dp(out_scale), _stream(stream)), "hq_rmsnorm")
+
+
+def hq_silu_mul_quant(dtype, out_dtype, a_scale, rows, I, gate_up, out, out_scale, stream=None) -> None:
+    _check(lib().hq_silu_mul_quant(dtype, out_dtype, a_scale, rows, I, _dp(gate_up), _dp(out), _dp(out_scale), _stream(stream)),
+           "hq_silu_mul_quant")
+
+
+def hq_moe_route(desc, T, logits, logits_stride, bias, topk_ids, topk_weights, stream=None) -> None:
+    _check(lib().hq_moe_route(C.byref(desc), T, _dp(logits), logits_stride, _dp(bias), _dp(topk_ids), _dp(topk_weights),
+                              _stream(stream)), "hq_moe_route")
+
+
+def hq_moe_combine(dtype, T, top_k, N, y, topk_weights, out, add=None, sorted_pairs=None, workspace=None, ws_bytes=0,
+                   stream=None) -> None:
+    _check(lib().hq_moe_combine(dtype, T, top_k, N, _dp(y), _dp(topk_weights), _dp(sorted_pairs), _dp(add), _dp(out),
+                                _dp(workspace), ws_bytes, _stream(stream)), "hq_moe_combine")
 
 
 def hq_kv_slots(block_size, B, T_cap, cached_lens, new_lens, free_blocks, n_free, block_table, max_blocks, cu_new, kv_lens,

@@ -18,6 +18,9 @@
  * Around a paged key/value cache: block tables and slot maps, rotary positions
  * with the cache write, and attention behind a prefix that requests share.
  *
+ * Around a routed layer's expert products: RMS norm and SwiGLU with quantised
+ * outputs, routing to experts, and the weighted sum over a token's experts.
+ *
  * Sources.  The operation and its parameters follow the Humming pages:
  *  - "Humming wird angekuendigt", section "Eine einheitliche
  *    Quantisierungsdarstellung": weights, scales, zero-points and second-level
@@ -178,6 +181,8 @@ typedef enum hq_moe_mode {
  *   BF16|FP16 FP4_E2M1   FP8_E4M3, PER_GROUP_K, grp 16 NONE    NONE      a_dtype (NVFP4; scale2
  *                                                                               PER_TENSOR_F32)
  *   BF16      FP4_E2M1   E8M0, PER_GROUP_K, group 32   NONE    NONE      BF16   (MoE)
+ *   FP8_E4M3  FP8_E4M3   FP32, BLOCK_128x128           NONE    PER_BLOCK128 BF16 (MoE; an expert's
+ *                                                                               weights below 2 GiB)
  *   BF16|FP16 INT4       E8M0, PER_GROUP_K, group 32   NONE    NONE      a_dtype (MXINT4)
  *   BF16|FP16 INT8       FP32, PER_CHANNEL             NONE    NONE      a_dtype (INT8 weight-only)
  *   BF16|FP16 FP8_E4M3   FP32, PER_CHANNEL             NONE    NONE      a_dtype (FP8 weight-only)
@@ -422,7 +427,13 @@ hq_status hq_gemm_plan(const hq_layer_desc* desc, int64_t M, char* buf, size_t l
  *            int32 [num_experts+1] (nondecreasing, offsets[0] = 0,
  *            offsets[E] = T*top_k); D [T*top_k][N] in the same row order.
  *            topk_ids must be NULL.
- * Routing weights are not applied.  T == 0 returns HQ_OK.
+ * Routing weights are not applied (hq_moe_combine does).  T == 0 returns HQ_OK.
+ * a_scale is for FP8 experts only: fp32, one per row of A and 128-K block,
+ * [rows of A][K/128]; their sums over K go block by block in order, in fp32, so a
+ * row's result does not depend on the other rows.  (As in every product of 8-bit
+ * floats here, the matrix instruction adds the products of 8 neighbouring K at 13 bits
+ * below the largest's power of two: about 2^-19 of the sum of absolute values.)  Rows of D whose id is outside
+ * 0..num_experts-1 are not written.
  */
 hq_status hq_moe_gemm(const hq_layer_desc* desc, int32_t mode, int64_t T, int32_t top_k,
                       const void* A, const float* a_scale, const int32_t* topk_ids,
@@ -503,10 +514,116 @@ hq_status hq_moe_align(int64_t T, int32_t top_k, int32_t num_experts, const int3
 
 /*
  * Builds the Grouped activation matrix: A_sorted[i] = A[sorted_pairs[i] / top_k]
- * for i < T*top_k; rows of K elements of `dtype` (BF16, FP16, FP8_E4M3, INT8).
+ * for i < T*top_k; rows of K elements of `dtype` (BF16, FP16, FP8_E4M3, INT8: row
+ * bytes a multiple of 16; FP32: any K, for the rows' scales).
  */
 hq_status hq_moe_gather(int32_t dtype, int64_t T, int32_t top_k, int64_t K, const void* A,
                         const int32_t* sorted_pairs, void* A_sorted, hq_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* a routed layer around its expert products (device)                       */
+/* ---------------------------------------------------------------------- */
+
+/*
+ * A mixture-of-experts layer is, in order: hq_rmsnorm (the residual's addition, the
+ * norm, the activations in 8 bits), a router's projection, hq_moe_route, hq_moe_gemm
+ * (gate and up), hq_silu_mul_quant, hq_moe_gemm (down: INDEXED with T = T * top_k,
+ * top_k = 1 and the same ids), hq_moe_combine.
+ *
+ * RMS norm of M rows of K elements:
+ *   h = x + residual (x alone without one),  sum_out = h rounded to dtype,
+ *   y = h / sqrt(mean(h^2) + eps) * (weight + weight_offset)
+ * in fp32 from the unrounded h, and y in one of these forms:
+ *   out_dtype   a_scale        out
+ *   dtype       NONE           [M][K], rounded once; out_scale NULL
+ *   FP8_E4M3    PER_TOKEN_F32  as hq_quantize_act: s = max|y| / 448 per row (1 for a row of zeros)
+ *   INT8        PER_TOKEN_F32  s = max|y| / 127, q = y / s to the nearest (ties to even) of -127..127; NaN gives 0
+ *   FP8_E4M3    PER_BLOCK128   as hq_quantize_act_blocks with block 128 (K a multiple of 128)
+ *   FP8_E4M3 | FP4_E2M1  MX_E8M0  as hq_quantize_act_mx (K a multiple of 32)
+ * which are the activations of the layers with that a_dtype and a_scale.  NaN and
+ * infinities of y go as they do there.
+ *   x, residual  device, dtype (BF16 or FP16), rows at their strides (elements, at
+ *                least K); residual may be NULL
+ *   weight       [K], weight_dtype: dtype or FP32
+ *   sum_out      dtype, or NULL; may be x or residual itself with the same stride
+ *   out          dense [M][K] (E2M1: [M][K/2] bytes); out_scale as the table says
+ * K 1..65536, M at most 2^22.  Rows and strides that are multiples of 8 are read 16
+ * bytes at a time; others are taken too, but not with block scales (128 or MX).
+ * Squares are summed in fp32: a row whose squares pass 2^127 in sum gives zeros (NaN
+ * where h is infinite).  Apart from sum_out the outputs must not overlap the inputs.
+ */
+typedef struct hq_norm_desc {
+    int32_t abi_version;  /* HQ_ABI_VERSION                      */
+    int32_t dtype;        /* x, residual, sum_out: BF16 or FP16  */
+    int32_t weight_dtype; /* dtype, or FP32                      */
+    int32_t out_dtype;    /* see above                           */
+    int32_t a_scale;      /* hq_ascale of the output             */
+    float eps;            /* finite, >= 0                        */
+    float weight_offset;  /* 0, or 1 for weights stored around 0 */
+    int32_t reserved;     /* must be zero                        */
+} hq_norm_desc;
+hq_status hq_rmsnorm(const hq_norm_desc* desc, int64_t M, int64_t K, const void* x, int64_t x_stride, const void* residual,
+                     int64_t residual_stride, const void* weight, void* sum_out, int64_t sum_stride, void* out,
+                     void* out_scale, hq_stream_t stream);
+
+/*
+ * SwiGLU with a quantised output: y = silu(gate) * up of rows gate | up ([rows][2I],
+ * dtype BF16 or FP16), fp32 as in hq_silu_mul, and y's codes and scales in any of
+ * the quantised forms of hq_rmsnorm.  I a multiple of 8 (of 128 or 32 for block
+ * scales), at most 65536; rows at most 2^22; the buffers must not overlap.
+ */
+hq_status hq_silu_mul_quant(int32_t dtype, int32_t out_dtype, int32_t a_scale, int64_t rows, int64_t I, const void* gate_up,
+                            void* out, void* out_scale, hq_stream_t stream);
+
+/*
+ * Routing: the top_k experts of each token and their weights, from the logits of
+ * num_experts experts.
+ *   scores   SOFTMAX s_e = e^(l_e - max l) / sum;  SIGMOID s_e = 1 / (1 + e^-l_e)
+ *   ranking  by c_e = s_e + bias_e; without a bias by the logits
+ *   groups   (groups > 1) of num_experts / groups neighbouring experts: only those of
+ *            the top_groups groups of the largest value can be chosen; a group's value
+ *            is the sum of its group_best (1 or 2) largest c_e (s_e without a bias)
+ *   chosen   the top_k largest of the ranking, in descending order
+ *   weights  scale * s_e, divided first by the sum of the chosen s_e if renormalize
+ * Scores are formed and compared in 64 bits, and equal values (of experts and of
+ * groups) go to the lowest index, so the ids are those of the formula.  NaN ranks
+ * lowest, with -inf (an expert of bias -inf is taken only where nothing else is
+ * left).  Softmax weights of a token whose logits are all -inf are 0, and
+ * renormalised weights whose sum is 0; a NaN logit makes every softmax weight of its
+ * token NaN.  The ids are distinct and inside 0..num_experts-1 in any case.
+ *   logits   device, dtype (FP32, BF16, FP16), row t at t * logits_stride (elements)
+ *   bias     fp32 [num_experts] or NULL
+ *   topk_ids int32 [T][top_k], topk_weights fp32 [T][top_k]
+ * num_experts 1..4096, groups 1..64 dividing it, top_k 1..64.
+ */
+typedef enum hq_route_scoring { HQ_ROUTE_SOFTMAX = 1, HQ_ROUTE_SIGMOID = 2 } hq_route_scoring;
+typedef struct hq_route_desc {
+    int32_t abi_version; /* HQ_ABI_VERSION              */
+    int32_t dtype;       /* of the logits               */
+    int32_t num_experts, top_k;
+    int32_t scoring;     /* hq_route_scoring            */
+    int32_t renormalize; /* 0 or 1                      */
+    int32_t groups, top_groups, group_best; /* 1, 1, 1: no groups */
+    float scale;         /* finite                      */
+    int32_t reserved;    /* must be zero                */
+} hq_route_desc;
+hq_status hq_moe_route(const hq_route_desc* desc, int64_t T, const void* logits, int64_t logits_stride, const float* bias,
+                       int32_t* topk_ids, float* topk_weights, hq_stream_t stream);
+
+/*
+ * out[t] = add[t] + sum_j topk_weights[t][j] * y[row of pair t*top_k + j], j in order,
+ * fp32 sums, add (the residual, a shared expert; or NULL) last, one rounding.
+ *   y       dtype (BF16 or FP16) [T*top_k][N]: row t*top_k + j (hq_moe_gemm INDEXED),
+ *           or, with sorted_pairs (hq_moe_align), row i holds pair sorted_pairs[i]
+ *   add, out  dtype [T][N]; out may be add itself
+ * A row whose weight is 0 is not read and adds nothing, whatever it holds; nor does a
+ * pair that sorted_pairs does not name (one named twice has either row).  workspace:
+ * T*top_k*4 bytes with sorted_pairs, else none.  N 1..2^21, T at most 2^23; rows of a
+ * multiple of 8 elements are read 16 bytes at a time.
+ */
+hq_status hq_moe_combine(int32_t dtype, int64_t T, int32_t top_k, int64_t N, const void* y, const float* topk_weights,
+                         const int32_t* sorted_pairs, const void* add, void* out, void* workspace, size_t ws_bytes,
+                         hq_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* paged key/value cache: slots, rotary positions, attention (device)       */
