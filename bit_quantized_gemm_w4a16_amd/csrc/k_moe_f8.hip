@@ -19,14 +19,18 @@
 #include "hq_device.hpp"
 #include "hq_layer.h"
 
+#include <type_traits>
+#include <utility>
+
 namespace hq {
 
 namespace {
 
 constexpr int kF8InlineP = 64;   // one pair per lane of a wave
 constexpr int kF8Chunk = 8192;   // pairs of one routing workgroup
-constexpr int kF8Rows = 64;      // rows of an m-tile
-constexpr int kF8Sa = 64;        // K blocks of activation scales in LDS at a time
+constexpr int kF8Rows = 64;      // an expert with at most so many rows is one m-tile of the weight stream
+constexpr int kF8TileRows = 256; // else m-tiles of at most so many, of 32 rows each way
+constexpr int kF8Sa = 64;        // K blocks of activation scales in LDS at a time (weight stream)
 
 size_t al16(size_t b) { return (b + 15) / 16 * 16; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -36,15 +40,21 @@ struct Tile {
 };
 
 struct F8Layout {  // byte offsets into the workspace
-    size_t hist, rank, offsets, sorted, tiles, ntiles, bytes;
-    int64_t max_tiles;
+    size_t hist, rank, offsets, sorted, tiles[2], ntiles, bytes;
+    int64_t max_tiles[2];  // bounds of the lists of the weight stream's m-tiles and of the others
+};
+struct F8Lists {
+    Tile* tiles[2];
+    int* ntiles;  // [2]
+    int max_tiles[2];
 };
 
 F8Layout f8_layout(int64_t T, int top_k, int E) {
     const int64_t P = T * top_k, C = ceil_div(P, kF8Chunk);
     F8Layout L{};
-    // an expert with c rows has ceil(c / kF8Rows) tiles
-    L.max_tiles = P / kF8Rows + (E < P ? E : P);
+    L.max_tiles[0] = E < P ? E : P;
+    const int64_t many = P / (kF8Rows + 1);  // experts that can have more rows
+    L.max_tiles[1] = P / kF8TileRows + (E < many ? E : many);
     size_t o = 0;
     L.hist = o;
     o += C > 1 ? al16((size_t)C * E * 4) : 0;
@@ -54,8 +64,10 @@ F8Layout f8_layout(int64_t T, int top_k, int E) {
     o += al16((size_t)(E + 1) * 4);
     L.sorted = o;
     o += al16((size_t)P * 4);
-    L.tiles = o;
-    o += al16((size_t)L.max_tiles * sizeof(Tile));
+    for (int i = 0; i < 2; ++i) {
+        L.tiles[i] = o;
+        o += al16((size_t)L.max_tiles[i] * sizeof(Tile));
+    }
     L.ntiles = o;
     o += 16;
     L.bytes = o;
@@ -66,65 +78,82 @@ F8Layout f8_layout(int64_t T, int top_k, int E) {
 // routing
 // ---------------------------------------------------------------------------
 
-// Exclusive scan of two values per thread over 1024 threads (tmp: 32 ints).
-__device__ void scan2_1024(int& a, int& b, int* tmp) {
+// Exclusive scan of three values per thread over 1024 threads (tmp: 48 ints).
+__device__ void scan3_1024(int (&v)[3], int* tmp) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    int ia = a, ib = b;
+    int incl[3];
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int oa = __shfl_up(ia, off), ob = __shfl_up(ib, off);
-        if (lane >= off) {
-            ia += oa;
-            ib += ob;
+    for (int i = 0; i < 3; ++i) {
+        incl[i] = v[i];
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int o = __shfl_up(incl[i], off);
+            if (lane >= off) incl[i] += o;
         }
     }
     __syncthreads();
-    if (lane == 63) {
-        tmp[wave] = ia;
-        tmp[16 + wave] = ib;
-    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (lane == 63) tmp[16 * i + wave] = incl[i];
     __syncthreads();
-    int ba = 0, bb = 0;
-    for (int w = 0; w < wave; ++w) {
-        ba += tmp[w];
-        bb += tmp[16 + w];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        int before = 0;
+        for (int w = 0; w < wave; ++w) before += tmp[16 * i + w];
+        v[i] = before + incl[i] - v[i];
     }
-    a = ba + ia - a;
-    b = bb + ib - b;
 }
 
-// Offsets (written to off[0..E], global or LDS) and the tile list from counts of at
+// How many m-tiles an expert of c rows has in a list, and how many rows each (the last
+// may have fewer): the tiles of a large expert are as even as 32 rows allow.
+__device__ __forceinline__ int f8_tiles(int c, int list) {
+    return c == 0 || (c <= kF8Rows) != (list == 0) ? 0 : list == 0 ? 1 : (c + kF8TileRows - 1) / kF8TileRows;
+}
+__device__ __forceinline__ int f8_tile_rows(int c) {
+    const int n = (c + kF8TileRows - 1) / kF8TileRows;
+    return c <= kF8Rows ? c : ((c + 31) / 32 + n - 1) / n * 32;
+}
+
+// Offsets (written to off[0..E-1], global or LDS) and the tile lists from counts of at
 // most 4096 experts, 4 per thread.
-__device__ void offsets_and_tiles(const int (&cnt)[4], const int (&first_of)[4], bool given, int E, int* off, Tile* tiles, int* ntiles,
-                                  int max_tiles, int* tmp) {
+__device__ void offsets_and_tiles(const int (&cnt)[4], const int (&first_of)[4], bool given, int E, int* off, const F8Lists& lists, int* tmp) {
     const int t = threadIdx.x;
-    int rows = 0, nt = 0;
+    int v[3] = {};  // rows, tiles of either list
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        rows += cnt[k];
-        nt += (cnt[k] + kF8Rows - 1) / kF8Rows;
+        v[0] += cnt[k];
+        v[1] += f8_tiles(cnt[k], 0);
+        v[2] += f8_tiles(cnt[k], 1);
     }
-    const int my_nt = nt;
-    scan2_1024(rows, nt, tmp);
-    if (t == 1023) *ntiles = min(nt + my_nt, max_tiles);
+    const int mine[2] = {v[1], v[2]};
+    scan3_1024(v, tmp);
+    if (t == 1023) {
+        lists.ntiles[0] = min(v[1] + mine[0], lists.max_tiles[0]);
+        lists.ntiles[1] = min(v[2] + mine[1], lists.max_tiles[1]);
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int e = 4 * t + k;
         if (e < E) {
-            const int start = given ? first_of[k] : rows;
+            const int start = given ? first_of[k] : v[0];
             if (off) off[e] = start;
-            for (int r = 0; r < cnt[k]; r += kF8Rows, ++nt)
-                if (nt < max_tiles) tiles[nt] = Tile{e, start + r, min(kF8Rows, cnt[k] - r)};
+            const int step = f8_tile_rows(cnt[k]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int n = f8_tiles(cnt[k], i);
+                for (int q = 0; q < n && v[1 + i] + q < lists.max_tiles[i]; ++q)
+                    lists.tiles[i][v[1 + i] + q] = Tile{e, start + q * step, min(step, cnt[k] - q * step)};
+                v[1 + i] += n;
+            }
         }
-        rows += cnt[k];
+        v[0] += cnt[k];
     }
 }
 
 // The whole routing of at most kF8Chunk pairs (Indexed).
-__global__ __launch_bounds__(1024) void f8_route_kernel(const int* __restrict__ ids, int P, int E, int* __restrict__ sorted, Tile* __restrict__ tiles,
-                                                        int* __restrict__ ntiles, int max_tiles) {
+__global__ __launch_bounds__(1024) void f8_route_kernel(const int* __restrict__ ids, int P, int E, int* __restrict__ sorted, F8Lists lists) {
     __shared__ int cnt[4096];
-    __shared__ int tmp[32];
+    __shared__ int tmp[48];
     const int t = threadIdx.x;
     for (int e = t; e < 4096; e += 1024) cnt[e] = 0;
     __syncthreads();
@@ -142,7 +171,7 @@ __global__ __launch_bounds__(1024) void f8_route_kernel(const int* __restrict__ 
 #pragma unroll
     for (int k = 0; k < 4; ++k) c[k] = cnt[4 * t + k];
     __syncthreads();
-    offsets_and_tiles(c, none, false, E, cnt, tiles, ntiles, max_tiles, tmp);
+    offsets_and_tiles(c, none, false, E, cnt, lists, tmp);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kF8Chunk / 1024; ++i)
@@ -165,8 +194,8 @@ __global__ __launch_bounds__(1024) void f8_hist_kernel(const int* __restrict__ i
 }
 // ... the scan over chunks and experts with the tile list (or the list alone, from given offsets), ...
 __global__ __launch_bounds__(1024) void f8_scan_kernel(int* __restrict__ hist, int C, const int* __restrict__ given, int64_t P, int E,
-                                                       int* __restrict__ off, Tile* __restrict__ tiles, int* __restrict__ ntiles, int max_tiles) {
-    __shared__ int tmp[32];
+                                                       int* __restrict__ off, F8Lists lists) {
+    __shared__ int tmp[48];
     const int t = threadIdx.x;
     int c[4], first[4] = {};
 #pragma unroll
@@ -185,7 +214,7 @@ __global__ __launch_bounds__(1024) void f8_scan_kernel(int* __restrict__ hist, i
             }
         }
     }
-    offsets_and_tiles(c, first, given != nullptr, E, given ? nullptr : off, tiles, ntiles, max_tiles, tmp);
+    offsets_and_tiles(c, first, given != nullptr, E, given ? nullptr : off, lists, tmp);
 }
 // ... and the placing.
 __global__ __launch_bounds__(256) void f8_place_kernel(const int* __restrict__ ids, int64_t P, int E, const int* __restrict__ hist,
@@ -219,10 +248,53 @@ struct F8Params {
     int P, E;
 };
 
+constexpr uint32_t kNone = 0x80000000u;  // past every weight and scale resource: reads zeros (of A: some byte, or zeros)
+constexpr int kF8SaRow = kF8Sa + 1;      // (one word more: the rows' scales of a block lie on different banks)
+
+// s_waitcnt vmcnt(N), the other counters left alone (gfx9 encoding).
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    static_assert(N >= 0 && N < 64, "vmcnt is a 6-bit counter");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+// Workgroup barriers for direct loads to LDS: a wave has waited for its own by then, and
+// __syncthreads() would wait for every load in flight.  lds_sync: for LDS writes too.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void lds_sync() {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    lds_barrier();
+}
+
 union F8Frag {
     v4u q[2];
     v8i v;
 };
+
+// One product of a block: 16 columns of weights as the MFMA's rows, 16 rows of A as its
+// columns.  So a lane's results belong to ONE row of A (column lane & 15 of the result):
+// the row's scale is one value per lane, and its four results are neighbouring columns
+// of D (4 (lane >> 4) .. + 3).
+__device__ __forceinline__ v4f f8_product(const F8Frag& w, const F8Frag& a) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, a.v, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7F, 0, 0x7F);
+}
+// Columns n .. n + 3 of row `row` of D (-1: none).
+__device__ __forceinline__ void f8_store(const F8Params& p, int row, int n, const v4f& v) {
+    if (row < 0) return;
+    uint16_t* d = p.D + (int64_t)row * p.N + n;
+    if (p.N % 4 == 0) {  // (then n + 3 < N wherever n < N, and the address is a multiple of 8)
+        if (n < p.N)
+            *(uint2*)d = make_uint2((uint32_t)f32_to_bf16_bits(v[0]) | ((uint32_t)f32_to_bf16_bits(v[1]) << 16),
+                                    (uint32_t)f32_to_bf16_bits(v[2]) | ((uint32_t)f32_to_bf16_bits(v[3]) << 16));
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (n + r < p.N) d[r] = f32_to_bf16_bits(v[r]);
+    }
+}
 
 // The products of one m-tile (MT x 16 rows) with 128 columns: four waves of two strips
 // (16 columns) each.  Every wave streams its weights from HBM to registers, PF blocks
@@ -238,8 +310,6 @@ __device__ __forceinline__ void f8_stream(const F8Params& p, const Tile& tile, i
     const rsrc_t rW = make_rsrc(p.W + (int64_t)tile.expert * p.w_estride, (uint32_t)p.w_estride);
     const rsrc_t rA = make_rsrc(p.A, (uint32_t)(p.a_rows * p.K));
     const rsrc_t rS = make_rsrc(p.S + (int64_t)tile.expert * p.s_estride, (uint32_t)(p.s_estride * 4));
-    constexpr uint32_t kNone = 0x80000000u;  // past every weight and scale resource: reads zeros
-    constexpr uint32_t kPast = 0x7F000000u;  // a block past K: zeros, or bytes that are not used
     uint32_t boff[NT], aoff[MT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -251,15 +321,16 @@ __device__ __forceinline__ void f8_stream(const F8Params& p, const Tile& tile, i
 
     F8Frag b[PF][NT], a[PF][MT];
     auto load = [&](int s, int blk) {
-        const bool ok = blk < nb;
+        const bool ok = blk < nb;  // (past K: nothing is fetched)
+        const uint32_t at = ok ? (uint32_t)blk : 0u;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) b[s][j].q[h] = buf16<true>(rW, boff[j], ok ? (uint32_t)blk * 2048u + h * 1024u : kPast);
+            for (int h = 0; h < 2; ++h) b[s][j].q[h] = buf16<true>(rW, ok ? boff[j] : kNone, at * 2048u + h * 1024u);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) a[s][i].q[h] = buf16(rA, aoff[i], ok ? (uint32_t)blk * 128u + h * 64u : kPast);
+            for (int h = 0; h < 2; ++h) a[s][i].q[h] = buf16(rA, ok ? aoff[i] : kNone, at * 128u + h * 64u);
     };
     v4f acc[MT][NT];
 #pragma unroll
@@ -271,29 +342,27 @@ __device__ __forceinline__ void f8_stream(const F8Params& p, const Tile& tile, i
 
     for (int b0 = 0; b0 < nb; b0 += kF8Sa) {
         const int n = min(nb - b0, kF8Sa);
-        // scales of the rows, [block][row]; lane l keeps the weight scale of block b0 + l
+        // scales of the rows; lane l keeps the weight scale of block b0 + l
         __syncthreads();
         for (int i = tid; i < MT * 16 * kF8Sa; i += 256) {
             const int r = i / kF8Sa, s = i % kF8Sa;
-            if (s < n) sal[s * (MT * 16) + r] = p.sa[(int64_t)rowA[r] * nb + b0 + s];
+            if (s < n) sal[r * kF8SaRow + s] = p.sa[(int64_t)rowA[r] * nb + b0 + s];
         }
         const float sw_lane = __uint_as_float(buf4(rS, lane < n ? (uint32_t)((b0 + lane) * p.ncb + cb) * 4u : kNone, 0u));
         __syncthreads();
         for (int s0 = 0; s0 < n; s0 += PF) {
 #pragma unroll
             for (int s = 0; s < PF; ++s) {
-                // blocks past K: their scales are not read, and nothing is added
-                const bool live = s0 + s < n;
-                const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw_lane), (s0 + s) & 63));
+                if (s0 + s < n) {  // (blocks past K add nothing)
+                    const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw_lane), s0 + s));
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    v4f sc = *(const v4f*)(sal + (live ? s0 + s : 0) * (MT * 16) + i * 16 + quad * 4);
+                    for (int i = 0; i < MT; ++i) {
+                        const float sc = sal[(i * 16 + col) * kF8SaRow + s0 + s] * sw;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[s][i].v, b[s][j].v, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7F, 0, 0x7F);
-                        if (live) {
+                        for (int j = 0; j < NT; ++j) {
+                            const v4f part = f8_product(b[s][j], a[s][i]);
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) acc[i][j][r] += part[r] * (sc[r] * sw);
+                            for (int r = 0; r < 4; ++r) acc[i][j][r] += part[r] * sc;
                         }
                     }
                 }
@@ -302,22 +371,14 @@ __device__ __forceinline__ void f8_stream(const F8Params& p, const Tile& tile, i
         }
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int n = (cb * 8 + wave * NT + j) * 16 + col;
-        if (n >= p.N) continue;
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = rowD[i * 16 + quad * 4 + r];
-                if (row >= 0) p.D[(int64_t)row * p.N + n] = f32_to_bf16_bits(acc[i][j][r]);
-            }
-    }
+        for (int i = 0; i < MT; ++i) f8_store(p, rowD[i * 16 + col], (cb * 8 + wave * NT + j) * 16 + quad * 4, acc[i][j]);
 }
 
 __global__ __launch_bounds__(256) void f8_stream_kernel(F8Params p) {
     __shared__ int rowA[kF8Rows], rowD[kF8Rows];
-    __shared__ __attribute__((aligned(16))) float sal[kF8Sa * kF8Rows];
+    __shared__ __attribute__((aligned(16))) float sal[kF8SaRow * kF8Rows];
     __shared__ int owner[kF8InlineP];
     const int tid = threadIdx.x, lane = tid & 63;
     const int cb = blockIdx.x % (unsigned)p.ncb, mt = blockIdx.x / (unsigned)p.ncb;  // column block, m-tile
@@ -375,6 +436,234 @@ __global__ __launch_bounds__(256) void f8_stream_kernel(F8Params p) {
     else f8_stream<4>(p, tile, cb, rowA, rowD, sal);
 }
 
+// ---- m-tiles of more rows: 256 x 256 of D on eight waves ----
+//
+// Wave (wm, wn) has the 16-row subtiles 2 i + wm (i < MT) and the columns 64 wn .. + 63.
+// Codes of rows and weights both go to LDS by direct loads: a CU takes 51 bytes a clock
+// from L2 that way, into registers 39 (measured), and LDS gives 214; with the weights
+// loaded to registers by each of the two waves that need them the tile ran at half the
+// rate.  Two stages of 64 KB fill the LDS, and are filled again piece by piece as they
+// come free, so that every piece has one and a half blocks' time to land:
+//   P(s), before the last subtile of block s - 1: the weights and the first rows of block
+//        s have landed, block s - 1 is read to its end; A2(s + 1) is asked for
+//   M(s), before subtile H - 1 of block s: its later rows (A2) have landed, its weights
+//        are in registers and its first rows (A1) read; A1(s + 2) and B(s + 2) are asked for
+// The rows' scales come four blocks at a time through registers, the weights' wait in a
+// lane each.
+constexpr int kF8Half = 128 * 128;  // bytes of A1 or A2 of a stage: 128 rows of a block
+
+struct F8Stage {
+    char *a1[2], *a2[2], *b[2];
+    float* sa;
+};
+
+template <int MT>
+__device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int tn, const int* rowA, const int* rowD, const F8Stage& st) {
+    constexpr int NT = 4, H = MT >= 6 ? 4 : 2;                       // strips of a wave; subtiles of A1
+    constexpr int L1 = H / 2, L2 = (MT - H + 1) / 2, LB = 4;         // loads of a block: 64 rows each, 8 KB each
+    constexpr int kSa = kF8TileRows * 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 2, wn = wave & 3, col = lane & 15, quad = lane >> 4;
+    const int nb = p.nb, cb = tn * 2 + (wn >> 1);
+    const rsrc_t rW = make_rsrc(p.W + (int64_t)tile.expert * p.w_estride, (uint32_t)p.w_estride);
+    const rsrc_t rA = make_rsrc(p.A, (uint32_t)(p.a_rows * p.K));
+    const rsrc_t rS = make_rsrc(p.S + (int64_t)tile.expert * p.s_estride, (uint32_t)(p.s_estride * 4));
+    const rsrc_t rSA = make_rsrc(p.sa, (uint32_t)(p.a_rows * nb * 4));
+    // 16-byte slot i * 512 + tid of A1 and A2 together: row slot / 8, and of it the unit
+    // slot % 8 ^ (row >> 1 & 7), which spreads the reads of 16 rows over the banks
+    uint32_t aoff[L1 + L2];
+#pragma unroll
+    for (int i = 0; i < L1 + L2; ++i) {
+        const int row = i * 64 + (tid >> 3), unit = (tid & 7) ^ ((row >> 1) & 7);
+        aoff[i] = (uint32_t)rowA[min(row, kF8TileRows - 1)] * (uint32_t)p.K + (uint32_t)unit * 16u;
+    }
+    // wave w loads the strips 2 w and 2 w + 1 (past the last: zeros, they lie behind the resource)
+    const uint32_t strip_bytes = (uint32_t)nb * 2048u, strip0 = (uint32_t)(tn * 16 + wave * 2) * strip_bytes, boff = (uint32_t)lane * 16u;
+    const uint32_t saoff = (uint32_t)rowA[min(tid, kF8TileRows - 1)] * (uint32_t)nb * 4u;
+    auto load_a1 = [&](int blk, auto s) {
+        lds_char* to = (lds_char*)st.a1[decltype(s)::value & 1] + wave * 1024;
+        const uint32_t at = (uint32_t)min(blk, nb - 1) * 128u;  // (past K: the last block again, not used)
+#pragma unroll
+        for (int i = 0; i < L1; ++i) dma16(rA, to + i * 8192, aoff[i], at);
+    };
+    auto load_a2 = [&](int blk, auto s) {
+        lds_char* to = (lds_char*)st.a2[decltype(s)::value & 1] + wave * 1024;
+        const uint32_t at = (uint32_t)min(blk, nb - 1) * 128u;
+#pragma unroll
+        for (int i = 0; i < L2; ++i) dma16(rA, to + i * 8192, aoff[L1 + i], at);
+    };
+    auto load_b = [&](int blk, auto s) {
+        lds_char* to = (lds_char*)st.b[decltype(s)::value & 1] + wave * 4096;
+        const uint32_t at = strip0 + (uint32_t)min(blk, nb - 1) * 2048u;
+#pragma unroll
+        for (int i = 0; i < LB; ++i) dma16(rW, to + i * 1024, boff, at + (i >> 1) * strip_bytes + (i & 1) * 1024u);
+    };
+    float acc[MT][NT][4] = {};
+    v4u sa_next = buf16(rSA, saoff, 0u);
+    float sw_lane = 0.f, sw = 0.f;
+    // this lane's operand of a subtile: units quad and 4 + quad of its row
+    const int f0 = (wm * 16 + col) * 128 + ((quad ^ ((col >> 1) & 7)) * 16), f1 = f0 ^ 64;
+    F8Frag a[2], b[NT];
+    float sa[2], sc = 0.f;
+    v4f part[4] = {};
+    auto read_a = [&](auto s, auto ic, int to) {  // subtile i of block s
+        constexpr int S = decltype(s)::value, i = decltype(ic)::value;
+        const char* A = i < H ? st.a1[S & 1] + i * 4096 : st.a2[S & 1] + (i - H) * 4096;
+        a[to].q[0] = *(const v4u*)(A + f0);
+        a[to].q[1] = *(const v4u*)(A + f1);
+    };
+    auto read_b = [&](auto s, int j) {
+        const char* B = st.b[decltype(s)::value & 1] + (wn * NT + j) * 2048 + lane * 16;
+        b[j].q[0] = *(const v4u*)B;
+        b[j].q[1] = *(const v4u*)(B + 1024);
+    };
+    // Block s: product k = 4 i + j, and the fp32 sum of the product before the last, so that
+    // no sum waits for its product (the last two of a block are summed in the next one).
+    auto block = [&](int s, const float* sal, const float* sal_next, float* sa_to, auto cur) {
+        constexpr int S = decltype(cur)::value;
+        using Next = std::integral_constant<int, S + 1>;
+        auto subtile = [&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            // (an odd MT swaps the two operand sets from block to block)
+            constexpr int now = (MT & 1) ? (i + S) & 1 : i & 1;
+            if constexpr (i == H - 1) {  // M(s)
+                wait_vmcnt<L1 + L2 + LB>();
+                lds_sync();
+                load_b(s + 2, cur);
+                load_a1(s + 2, cur);
+                if constexpr (S == 0) sa_next = buf16(rSA, saoff, (uint32_t)min(s + 4, nb - 1) * 4u);
+            }
+            if constexpr (i == MT - 1) {  // P(s + 1)
+                wait_vmcnt<L1 + L2 + LB>();
+                if constexpr (S == 3)
+                    if (tid < kF8TileRows) *(v4u*)(sa_to + tid * 4) = sa_next;
+                lds_sync();
+                load_a2(s + 2, cur);
+                read_a(Next{}, std::integral_constant<int, 0>{}, now ^ 1);
+                sa[now ^ 1] = S < 3 ? sal[S + 1] : sal_next[0];
+            } else {
+                read_a(cur, std::integral_constant<int, i + 1>{}, now ^ 1);
+                sa[now ^ 1] = sal[(i + 1) * 128 + S];
+            }
+            if constexpr (i == 0) sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw_lane), s & 63));
+            const float before = sc;
+            sc = sa[now] * sw;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                // product (i, j); sum of (i, j - 2), or of the subtile before
+                float(&sum)[4] = j >= 2 ? acc[i][j - 2] : acc[i > 0 ? i - 1 : MT - 1][j + NT - 2];
+                part[j & 3] = f8_product(b[j], a[now]);
+                if constexpr (i == MT - 1) read_b(Next{}, j);
+                const float c = j >= 2 ? sc : before;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sum[r] += part[(j + 2) & 3][r] * c;
+                // the sum is wanted now: without this the products of several blocks are put
+                // off behind the loads that follow, and their operands do not fit the registers
+                asm volatile("" : "+v"(sum[0]), "+v"(sum[1]), "+v"(sum[2]), "+v"(sum[3]));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        auto all = [&]<int... I>(std::integer_sequence<int, I...>) { (subtile(std::integral_constant<int, I>{}), ...); };
+        all(std::make_integer_sequence<int, MT>{});
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    using S2 = std::integral_constant<int, 2>;
+    using S3 = std::integral_constant<int, 3>;
+    load_b(0, S0{});
+    load_a1(0, S0{});
+    load_a2(0, S0{});
+    load_b(1, S1{});
+    load_a1(1, S1{});
+    if (tid < kF8TileRows) *(v4u*)(st.sa + tid * 4) = sa_next;
+    wait_vmcnt<L1 + L2 + LB>();  // P(0)
+    lds_sync();
+    load_a2(1, S1{});
+    const float* sal = st.sa + (wm * 16 + col) * 4;
+    read_a(S0{}, S0{}, 0);
+    sa[0] = sal[0];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) read_b(S0{}, j);
+    // four blocks a turn, without branches between them (across one the compiler moves the
+    // products behind the loads that follow), then the last one to three
+    int s = 0;
+    auto scales = [&](float*& to, const float*& here, const float*& next) {
+        const int now = (s >> 2) & 1;  // which of the two buffers
+        here = sal + now * kSa;
+        next = sal + (now ^ 1) * kSa;
+        to = st.sa + (now ^ 1) * kSa;
+        if ((s & 63) == 0) {
+            sw_lane = __uint_as_float(buf4(rS, s + lane < nb ? (uint32_t)((s + lane) * p.ncb + cb) * 4u : kNone, 0u));
+            asm volatile("" : "+v"(sw_lane));  // (waited for here, not at each use)
+        }
+    };
+    float* to;
+    const float *here, *next;
+    for (; s + 4 <= nb; s += 4) {
+        scales(to, here, next);
+        block(s, here, next, to, S0{});
+        block(s + 1, here, next, to, S1{});
+        block(s + 2, here, next, to, S2{});
+        block(s + 3, here, next, to, S3{});
+    }
+    if (s < nb) {
+        scales(to, here, next);
+        block(s, here, next, to, S0{});
+        if (s + 1 < nb) block(s + 1, here, next, to, S1{});
+        if (s + 2 < nb) block(s + 2, here, next, to, S2{});
+    }
+#pragma unroll
+    for (int j = NT - 2; j < NT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[MT - 1][j][r] += part[j & 3][r] * sc;
+    wait_vmcnt<0>();  // no direct load is in flight when the workgroup ends
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int row = rowD[(2 * i + wm) * 16 + col];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) f8_store(p, row, tn * 256 + wn * 64 + j * 16 + quad * 4, v4f{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]});
+    }
+}
+
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_tile_kernel(F8Params p) {
+    // (an array for each piece: the compiler then knows that a direct load into one does not
+    // touch what is read from another)
+    __shared__ __attribute__((aligned(1024))) char a10[kF8Half], a11[kF8Half], a20[kF8Half], a21[kF8Half], b0[2 * kF8Half], b1[2 * kF8Half];
+    __shared__ __attribute__((aligned(16))) float sas[2 * kF8TileRows * 4];
+    __shared__ int rowA[kF8TileRows], rowD[kF8TileRows];
+    const F8Stage st{{a10, a11}, {a20, a21}, {b0, b1}, sas};
+    // workgroups go round the 8 XCDs: neighbouring tiles to one of them.  The m-tiles of an
+    // expert run side by side, so that its weights are read once into an XCD's L2
+    const int tiles_n = (p.N + 255) / 256, total = p.ntiles[1] * tiles_n;
+    int id = blockIdx.x;
+    if (id >= total) return;
+    id = (id & 7) * (total >> 3) + min(id & 7, total & 7) + (id >> 3);
+    const int group = 4 * tiles_n;  // four m-tiles, all columns
+    const int first = id / group * 4, gm = min(4, p.ntiles[1] - first);
+    const int mt = first + id % group % gm, tn = id % group / gm;
+    Tile tile = p.tiles[mt];
+    tile.expert = __builtin_amdgcn_readfirstlane(tile.expert);
+    tile.rows = __builtin_amdgcn_readfirstlane(tile.rows);
+    const int tid = threadIdx.x;
+    if (tid < kF8TileRows) {
+        const int pos = tile.first + min(tid, tile.rows - 1);
+        const int pair = p.sorted ? p.sorted[pos] : pos;
+        rowA[tid] = p.sorted ? pair / p.top_k : pos;
+        rowD[tid] = tid < tile.rows ? pair : -1;
+    }
+    __syncthreads();
+    switch ((tile.rows + 31) / 32) {
+        case 1:
+        case 2:
+        case 3: return f8_tile<3>(p, tile, tn, rowA, rowD, st);
+        case 4: return f8_tile<4>(p, tile, tn, rowA, rowD, st);
+        case 5: return f8_tile<5>(p, tile, tn, rowA, rowD, st);
+        case 6: return f8_tile<6>(p, tile, tn, rowA, rowD, st);
+        case 7: return f8_tile<7>(p, tile, tn, rowA, rowD, st);
+        default: return f8_tile<8>(p, tile, tn, rowA, rowD, st);
+    }
+}
+
 }  // namespace
 
 size_t moe_f8_workspace(int64_t T, int top_k, int E) {
@@ -402,37 +691,45 @@ hipError_t moe_f8_launch(const MoeF8Args& a) {
     p.top_k = a.top_k;
     p.P = (int)P;
     p.E = a.E;
-    int64_t tiles = L.max_tiles;
     hipError_t e = hipSuccess;
     if (P <= kF8InlineP) {
         p.ids = a.indexed ? a.ids : nullptr;
         p.offsets = a.indexed ? nullptr : a.offsets;
-        tiles = a.E < P ? a.E : P;
-    } else {
-        int* off = (int*)(ws + L.offsets);
-        int* sorted = (int*)(ws + L.sorted);
-        Tile* list = (Tile*)(ws + L.tiles);
-        int* ntiles = (int*)(ws + L.ntiles);
-        const int C = (int)ceil_div(P, kF8Chunk);
-        if (!a.indexed) {
-            hipLaunchKernelGGL(f8_scan_kernel, dim3(1), dim3(1024), 0, a.stream, (int*)nullptr, 0, a.offsets, P, a.E, (int*)nullptr, list, ntiles, (int)L.max_tiles);
-        } else if (C == 1) {
-            hipLaunchKernelGGL(f8_route_kernel, dim3(1), dim3(1024), 0, a.stream, a.ids, (int)P, a.E, sorted, list, ntiles, (int)L.max_tiles);
-        } else {
-            int *hist = (int*)(ws + L.hist), *rank = (int*)(ws + L.rank);
-            hipLaunchKernelGGL(f8_hist_kernel, dim3((unsigned)C), dim3(1024), 0, a.stream, a.ids, P, a.E, hist, rank);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-            hipLaunchKernelGGL(f8_scan_kernel, dim3(1), dim3(1024), 0, a.stream, hist, C, (const int*)nullptr, P, a.E, off, list, ntiles, (int)L.max_tiles);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-            hipLaunchKernelGGL(f8_place_kernel, dim3((unsigned)ceil_div(P, 256)), dim3(256), 0, a.stream, a.ids, P, a.E, (const int*)hist, (const int*)off,
-                               (const int*)rank, sorted);
-        }
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        p.tiles = list;
-        p.ntiles = ntiles;
-        p.sorted = a.indexed ? sorted : nullptr;
+        hipLaunchKernelGGL(f8_stream_kernel, dim3((unsigned)(L.max_tiles[0] * p.ncb)), dim3(256), 0, a.stream, p);
+        return hipGetLastError();
     }
-    hipLaunchKernelGGL(f8_stream_kernel, dim3((unsigned)(tiles * p.ncb)), dim3(256), 0, a.stream, p);
+    int* off = (int*)(ws + L.offsets);
+    int* sorted = (int*)(ws + L.sorted);
+    F8Lists lists{};
+    for (int i = 0; i < 2; ++i) {
+        lists.tiles[i] = (Tile*)(ws + L.tiles[i]);
+        lists.max_tiles[i] = (int)L.max_tiles[i];
+    }
+    lists.ntiles = (int*)(ws + L.ntiles);
+    const int C = (int)ceil_div(P, kF8Chunk);
+    if (!a.indexed) {
+        hipLaunchKernelGGL(f8_scan_kernel, dim3(1), dim3(1024), 0, a.stream, (int*)nullptr, 0, a.offsets, P, a.E, (int*)nullptr, lists);
+    } else if (C == 1) {
+        hipLaunchKernelGGL(f8_route_kernel, dim3(1), dim3(1024), 0, a.stream, a.ids, (int)P, a.E, sorted, lists);
+    } else {
+        int *hist = (int*)(ws + L.hist), *rank = (int*)(ws + L.rank);
+        hipLaunchKernelGGL(f8_hist_kernel, dim3((unsigned)C), dim3(1024), 0, a.stream, a.ids, P, a.E, hist, rank);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        hipLaunchKernelGGL(f8_scan_kernel, dim3(1), dim3(1024), 0, a.stream, hist, C, (const int*)nullptr, P, a.E, off, lists);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        hipLaunchKernelGGL(f8_place_kernel, dim3((unsigned)ceil_div(P, 256)), dim3(256), 0, a.stream, a.ids, P, a.E, (const int*)hist, (const int*)off,
+                           (const int*)rank, sorted);
+    }
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    p.ntiles = lists.ntiles;
+    p.sorted = a.indexed ? sorted : nullptr;
+    if (L.max_tiles[1] > 0) {
+        p.tiles = lists.tiles[1];
+        hipLaunchKernelGGL(f8_tile_kernel, dim3((unsigned)(L.max_tiles[1] * ceil_div(a.N, 256))), dim3(512), 0, a.stream, p);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    p.tiles = lists.tiles[0];
+    hipLaunchKernelGGL(f8_stream_kernel, dim3((unsigned)(L.max_tiles[0] * p.ncb)), dim3(256), 0, a.stream, p);
     return hipGetLastError();
 }
 
