@@ -279,7 +279,7 @@ union F8Frag {
 // the row's scale is one value per lane, and its four results are neighbouring columns
 // of D (4 (lane >> 4) .. + 3).
 __device__ __forceinline__ v4f f8_product(const F8Frag& w, const F8Frag& a) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, a.v, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7F, 0, 0x7F);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, a.v, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);  // (no scales: the unscaled form)
 }
 // Columns n .. n + 3 of row `row` of D (-1: none).
 __device__ __forceinline__ void f8_store(const F8Params& p, int row, int n, const v4f& v) {
@@ -480,23 +480,17 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int
     // wave w loads the strips 2 w and 2 w + 1 (past the last: zeros, they lie behind the resource)
     const uint32_t strip_bytes = (uint32_t)nb * 2048u, strip0 = (uint32_t)(tn * 16 + wave * 2) * strip_bytes, boff = (uint32_t)lane * 16u;
     const uint32_t saoff = (uint32_t)rowA[min(tid, kF8TileRows - 1)] * (uint32_t)nb * 4u;
-    auto load_a1 = [&](int blk, auto s) {
-        lds_char* to = (lds_char*)st.a1[decltype(s)::value & 1] + wave * 1024;
-        const uint32_t at = (uint32_t)min(blk, nb - 1) * 128u;  // (past K: the last block again, not used)
-#pragma unroll
-        for (int i = 0; i < L1; ++i) dma16(rA, to + i * 8192, aoff[i], at);
+    // load n of the L1 + LB that M asks for (weights first), or of P's L2; past K the last
+    // block again, not used
+    auto load_m = [&](int blk, int s, int n) {
+        const int at = min(blk, nb - 1);
+        if (n < LB)
+            dma16(rW, (lds_char*)st.b[s] + wave * 4096 + n * 1024, boff, strip0 + (uint32_t)at * 2048u + (n >> 1) * strip_bytes + (n & 1) * 1024u);
+        else
+            dma16(rA, (lds_char*)st.a1[s] + wave * 1024 + (n - LB) * 8192, aoff[n - LB], (uint32_t)at * 128u);
     };
-    auto load_a2 = [&](int blk, auto s) {
-        lds_char* to = (lds_char*)st.a2[decltype(s)::value & 1] + wave * 1024;
-        const uint32_t at = (uint32_t)min(blk, nb - 1) * 128u;
-#pragma unroll
-        for (int i = 0; i < L2; ++i) dma16(rA, to + i * 8192, aoff[L1 + i], at);
-    };
-    auto load_b = [&](int blk, auto s) {
-        lds_char* to = (lds_char*)st.b[decltype(s)::value & 1] + wave * 4096;
-        const uint32_t at = strip0 + (uint32_t)min(blk, nb - 1) * 2048u;
-#pragma unroll
-        for (int i = 0; i < LB; ++i) dma16(rW, to + i * 1024, boff, at + (i >> 1) * strip_bytes + (i & 1) * 1024u);
+    auto load_p = [&](int blk, int s, int n) {
+        dma16(rA, (lds_char*)st.a2[s] + wave * 1024 + n * 8192, aoff[L1 + n], (uint32_t)min(blk, nb - 1) * 128u);
     };
     float acc[MT][NT][4] = {};
     v4u sa_next = buf16(rSA, saoff, 0u);
@@ -529,8 +523,6 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int
             if constexpr (i == H - 1) {  // M(s)
                 wait_vmcnt<L1 + L2 + LB>();
                 lds_sync();
-                load_b(s + 2, cur);
-                load_a1(s + 2, cur);
                 if constexpr (S == 0) sa_next = buf16(rSA, saoff, (uint32_t)min(s + 4, nb - 1) * 4u);
             }
             if constexpr (i == MT - 1) {  // P(s + 1)
@@ -538,7 +530,6 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int
                 if constexpr (S == 3)
                     if (tid < kF8TileRows) *(v4u*)(sa_to + tid * 4) = sa_next;
                 lds_sync();
-                load_a2(s + 2, cur);
                 read_a(Next{}, std::integral_constant<int, 0>{}, now ^ 1);
                 sa[now ^ 1] = S < 3 ? sal[S + 1] : sal_next[0];
             } else {
@@ -554,6 +545,16 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int
                 float(&sum)[4] = j >= 2 ? acc[i][j - 2] : acc[i > 0 ? i - 1 : MT - 1][j + NT - 2];
                 part[j & 3] = f8_product(b[j], a[now]);
                 if constexpr (i == MT - 1) read_b(Next{}, j);
+                // the loads that the last barrier allows, a few with each product
+                const int since = i == MT - 1 ? j : (i - (H - 1)) * NT + j;
+                if constexpr (i == MT - 1) {
+                    if (since < L2) load_p(s + 2, S & 1, since);
+                } else if constexpr (i >= H - 1) {
+                    constexpr int each = (L1 + LB + (MT - H) * NT - 1) / ((MT - H) * NT);
+#pragma unroll
+                    for (int n = since * each; n < since * each + each; ++n)
+                        if (n < L1 + LB) load_m(s + 2, S & 1, n);
+                }
                 const float c = j >= 2 ? sc : before;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) sum[r] += part[(j + 2) & 3][r] * c;
@@ -570,15 +571,17 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int
     using S1 = std::integral_constant<int, 1>;
     using S2 = std::integral_constant<int, 2>;
     using S3 = std::integral_constant<int, 3>;
-    load_b(0, S0{});
-    load_a1(0, S0{});
-    load_a2(0, S0{});
-    load_b(1, S1{});
-    load_a1(1, S1{});
+#pragma unroll
+    for (int n = 0; n < L1 + LB; ++n) load_m(0, 0, n);
+#pragma unroll
+    for (int n = 0; n < L2; ++n) load_p(0, 0, n);
+#pragma unroll
+    for (int n = 0; n < L1 + LB; ++n) load_m(1, 1, n);
     if (tid < kF8TileRows) *(v4u*)(st.sa + tid * 4) = sa_next;
     wait_vmcnt<L1 + L2 + LB>();  // P(0)
     lds_sync();
-    load_a2(1, S1{});
+#pragma unroll
+    for (int n = 0; n < L2; ++n) load_p(1, 1, n);
     const float* sal = st.sa + (wm * 16 + col) * 4;
     read_a(S0{}, S0{}, 0);
     sa[0] = sal[0];
