@@ -35,8 +35,10 @@ constexpr int kF8Sa = 64;        // K blocks of activation scales in LDS at a ti
 size_t al16(size_t b) { return (b + 15) / 16 * 16; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// An m-tile: `rows` sorted rows from `first`.  In the list of the larger ones: all rows of
+// the expert, and the number of the tile among the expert's.
 struct Tile {
-    int expert, first, rows;
+    int expert, first, rows, number;
 };
 
 struct F8Layout {  // byte offsets into the workspace
@@ -137,12 +139,11 @@ __device__ void offsets_and_tiles(const int (&cnt)[4], const int (&first_of)[4],
         if (e < E) {
             const int start = given ? first_of[k] : v[0];
             if (off) off[e] = start;
-            const int step = f8_tile_rows(cnt[k]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int n = f8_tiles(cnt[k], i);
                 for (int q = 0; q < n && v[1 + i] + q < lists.max_tiles[i]; ++q)
-                    lists.tiles[i][v[1 + i] + q] = Tile{e, start + q * step, min(step, cnt[k] - q * step)};
+                    lists.tiles[i][v[1 + i] + q] = Tile{e, start, cnt[k], q};
                 v[1 + i] += n;
             }
         }
@@ -409,7 +410,7 @@ __global__ __launch_bounds__(256) void f8_stream_kernel(F8Params p) {
         const uint64_t mine = __ballot(id >= 0 && before == 0 && t == mt);
         const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(mine));
         const uint64_t rows = __ballot(id == e);
-        tile = Tile{e, 0, (int)__popcll(rows)};
+        tile = Tile{e, 0, (int)__popcll(rows), 0};
         if (tid < kF8Rows) {
             rowD[lane] = -1;
             rowA[lane] = p.ids ? __builtin_ctzll(rows) / p.top_k : __builtin_ctzll(rows);
@@ -450,6 +451,7 @@ __global__ __launch_bounds__(256) void f8_stream_kernel(F8Params p) {
 //        are in registers and its first rows (A1) read; A1(s + 2) and B(s + 2) are asked for
 // The rows' scales come four blocks at a time through registers, the weights' wait in a
 // lane each.
+constexpr int kF8Group = 6;
 constexpr int kF8Half = 128 * 128;  // bytes of A1 or A2 of a stage: 128 rows of a block
 
 struct F8Stage {
@@ -635,18 +637,20 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     __shared__ __attribute__((aligned(16))) float sas[2 * kF8TileRows * 4];
     __shared__ int rowA[kF8TileRows], rowD[kF8TileRows];
     const F8Stage st{{a10, a11}, {a20, a21}, {b0, b1}, sas};
-    // workgroups go round the 8 XCDs: neighbouring tiles to one of them.  The m-tiles of an
-    // expert run side by side, so that its weights are read once into an XCD's L2
+    // Workgroups go round the 8 XCDs: neighbouring tiles to one of them.  Some 32 run on an
+    // XCD at a time, and what they read in common comes into its L2 once: so up to kF8Group
+    // m-tiles of one expert run side by side, for one 256 columns after the other
     const int tiles_n = (p.N + 255) / 256, total = p.ntiles[1] * tiles_n;
     int id = blockIdx.x;
     if (id >= total) return;
     id = (id & 7) * (total >> 3) + min(id & 7, total & 7) + (id >> 3);
-    const int group = 4 * tiles_n;  // four m-tiles, all columns
-    const int first = id / group * 4, gm = min(4, p.ntiles[1] - first);
-    const int mt = first + id % group % gm, tn = id % group / gm;
-    Tile tile = p.tiles[mt];
+    Tile tile = p.tiles[id / tiles_n];  // a tile of the same group
     tile.expert = __builtin_amdgcn_readfirstlane(tile.expert);
-    tile.rows = __builtin_amdgcn_readfirstlane(tile.rows);
+    const int count = __builtin_amdgcn_readfirstlane(tile.rows), step = f8_tile_rows(count), number = __builtin_amdgcn_readfirstlane(tile.number);
+    const int group = number / kF8Group * kF8Group, n = min(kF8Group, f8_tiles(count, 1) - group);
+    const int in_group = id - (id / tiles_n - (number - group)) * tiles_n, tn = in_group / n, m = group + in_group % n;
+    tile.first += m * step;
+    tile.rows = min(step, count - m * step);
     const int tid = threadIdx.x;
     if (tid < kF8TileRows) {
         const int pos = tile.first + min(tid, tile.rows - 1);
