@@ -13,9 +13,11 @@
 // The rows of an expert are cut into m-tiles (expert, first sorted row, rows).
 // Routing: up to kF8InlineP pairs, each workgroup finds its m-tile from the ids or
 // the offsets by itself; above, a counting sort by expert and the tile list come
-// first (one workgroup up to kF8Chunk pairs, else histograms of chunks, a scan and
-// the placing).  Rows of an expert come in any order: a row's sums do not depend on
-// its place.
+// first: one workgroup up to kF8Chunk pairs, else histograms of chunks in one launch,
+// and a second in which each chunk's workgroup sums the histograms for itself and
+// places its pairs (32760 pairs: 11 us; with launches of their own for the scan and the
+// ranks 17).  Rows of an expert come in any order: a row's sums do not depend on its
+// place.
 #include "hq_device.hpp"
 #include "hq_layer.h"
 
@@ -27,7 +29,7 @@ namespace hq {
 namespace {
 
 constexpr int kF8InlineP = 64;   // one pair per lane of a wave
-constexpr int kF8Chunk = 8192;   // pairs of one routing workgroup
+constexpr int kF8Chunk = 4096;   // pairs of one routing workgroup
 constexpr int kF8Rows = 64;      // an expert with at most so many rows is one m-tile of the weight stream
 constexpr int kF8TileRows = 256; // else m-tiles of at most so many, of 32 rows each way
 constexpr int kF8Sa = 64;        // K blocks of activation scales in LDS at a time (weight stream)
@@ -42,7 +44,7 @@ struct Tile {
 };
 
 struct F8Layout {  // byte offsets into the workspace
-    size_t hist, rank, offsets, sorted, tiles[2], ntiles, bytes;
+    size_t hist, sorted, tiles[2], ntiles, bytes;
     int64_t max_tiles[2];  // bounds of the lists of the weight stream's m-tiles and of the others
 };
 struct F8Lists {
@@ -60,10 +62,6 @@ F8Layout f8_layout(int64_t T, int top_k, int E) {
     size_t o = 0;
     L.hist = o;
     o += C > 1 ? al16((size_t)C * E * 4) : 0;
-    L.rank = o;
-    o += C > 1 ? al16((size_t)P * 4) : 0;
-    L.offsets = o;
-    o += al16((size_t)(E + 1) * 4);
     L.sorted = o;
     o += al16((size_t)P * 4);
     for (int i = 0; i < 2; ++i) {
@@ -116,9 +114,9 @@ __device__ __forceinline__ int f8_tile_rows(int c) {
     return c <= kF8Rows ? c : ((c + 31) / 32 + n - 1) / n * 32;
 }
 
-// Offsets (written to off[0..E-1], global or LDS) and the tile lists from counts of at
-// most 4096 experts, 4 per thread.
-__device__ void offsets_and_tiles(const int (&cnt)[4], const int (&first_of)[4], bool given, int E, int* off, const F8Lists& lists, int* tmp) {
+// Where the experts' rows begin (in start), and the tile lists (where `list`), from the
+// counts of at most 4096 experts, 4 per thread; `given`: start holds it already.
+__device__ void offsets_and_tiles(const int (&cnt)[4], int (&start)[4], bool given, bool list, int E, const F8Lists& lists, int* tmp) {
     const int t = threadIdx.x;
     int v[3] = {};  // rows, tiles of either list
 #pragma unroll
@@ -129,7 +127,7 @@ __device__ void offsets_and_tiles(const int (&cnt)[4], const int (&first_of)[4],
     }
     const int mine[2] = {v[1], v[2]};
     scan3_1024(v, tmp);
-    if (t == 1023) {
+    if (list && t == 1023) {
         lists.ntiles[0] = min(v[1] + mine[0], lists.max_tiles[0]);
         lists.ntiles[1] = min(v[2] + mine[1], lists.max_tiles[1]);
     }
@@ -137,13 +135,12 @@ __device__ void offsets_and_tiles(const int (&cnt)[4], const int (&first_of)[4],
     for (int k = 0; k < 4; ++k) {
         const int e = 4 * t + k;
         if (e < E) {
-            const int start = given ? first_of[k] : v[0];
-            if (off) off[e] = start;
+            if (!given) start[k] = v[0];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int n = f8_tiles(cnt[k], i);
-                for (int q = 0; q < n && v[1 + i] + q < lists.max_tiles[i]; ++q)
-                    lists.tiles[i][v[1 + i] + q] = Tile{e, start, cnt[k], q};
+                for (int q = 0; list && q < n && v[1 + i] + q < lists.max_tiles[i]; ++q)
+                    lists.tiles[i][v[1 + i] + q] = Tile{e, start[k], cnt[k], q};
                 v[1 + i] += n;
             }
         }
@@ -151,79 +148,75 @@ __device__ void offsets_and_tiles(const int (&cnt)[4], const int (&first_of)[4],
     }
 }
 
-// The whole routing of at most kF8Chunk pairs (Indexed).
-__global__ __launch_bounds__(1024) void f8_route_kernel(const int* __restrict__ ids, int P, int E, int* __restrict__ sorted, F8Lists lists) {
-    __shared__ int cnt[4096];
-    __shared__ int tmp[48];
+constexpr int kF8Each = kF8Chunk / 1024;  // pairs of a thread
+
+// The ids of this thread's pairs (-1: none, or outside), and (where `count`) their counts in cnt[0..4095].
+__device__ __forceinline__ void f8_count(const int* ids, int64_t P, int E, bool count, int* cnt, int (&id)[kF8Each]) {
     const int t = threadIdx.x;
-    for (int e = t; e < 4096; e += 1024) cnt[e] = 0;
-    __syncthreads();
-    int id[kF8Chunk / 1024], rank[kF8Chunk / 1024];
+    const int64_t p0 = (int64_t)blockIdx.x * kF8Chunk + t;
 #pragma unroll
-    for (int i = 0; i < kF8Chunk / 1024; ++i) {
-        const int p = i * 1024 + t;
-        const int v = p < P ? ids[p] : -1;
+    for (int i = 0; i < kF8Each; ++i) {
+        const int v = p0 + i * 1024 < P ? ids[p0 + i * 1024] : -1;
         id[i] = v >= 0 && v < E ? v : -1;
     }
-#pragma unroll
-    for (int i = 0; i < kF8Chunk / 1024; ++i) rank[i] = id[i] >= 0 ? atomicAdd(&cnt[id[i]], 1) : 0;
-    __syncthreads();
-    int c[4], none[4] = {};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) c[k] = cnt[4 * t + k];
-    __syncthreads();
-    offsets_and_tiles(c, none, false, E, cnt, lists, tmp);
+    if (!count) return;
+    for (int e = t; e < 4096; e += 1024) cnt[e] = 0;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kF8Chunk / 1024; ++i)
-        if (id[i] >= 0) sorted[cnt[id[i]] + rank[i]] = i * 1024 + t;
+    for (int i = 0; i < kF8Each; ++i)
+        if (id[i] >= 0) atomicAdd(&cnt[id[i]], 1);
+    __syncthreads();
 }
 
-// Several chunks: counts and ranks of each chunk, ...
-__global__ __launch_bounds__(1024) void f8_hist_kernel(const int* __restrict__ ids, int64_t P, int E, int* __restrict__ hist, int* __restrict__ rank) {
+// Several chunks: the counts of each, ...
+__global__ __launch_bounds__(1024) void f8_hist_kernel(const int* __restrict__ ids, int64_t P, int E, int* __restrict__ hist) {
     __shared__ int cnt[4096];
-    const int t = threadIdx.x;
-    for (int e = t; e < E; e += 1024) cnt[e] = 0;
-    __syncthreads();
-    for (int i = t; i < kF8Chunk; i += 1024) {
-        const int64_t p = (int64_t)blockIdx.x * kF8Chunk + i;
-        const int v = p < P ? ids[p] : -1;
-        if (v >= 0 && v < E) rank[p] = atomicAdd(&cnt[v], 1);
-    }
-    __syncthreads();
-    for (int e = t; e < E; e += 1024) hist[(int64_t)blockIdx.x * E + e] = cnt[e];
+    int id[kF8Each];
+    f8_count(ids, P, E, true, cnt, id);
+    for (int e = threadIdx.x; e < E; e += 1024) hist[(int64_t)blockIdx.x * E + e] = cnt[e];
 }
-// ... the scan over chunks and experts with the tile list (or the list alone, from given offsets), ...
-__global__ __launch_bounds__(1024) void f8_scan_kernel(int* __restrict__ hist, int C, const int* __restrict__ given, int64_t P, int E,
-                                                       int* __restrict__ off, F8Lists lists) {
+// ... and the places of its pairs, behind the experts before theirs and the chunks before its own.  One
+// chunk (hist NULL): all in one launch.  The tile lists come from the first workgroup.
+__global__ __launch_bounds__(1024) void f8_place_kernel(const int* __restrict__ ids, int64_t P, int E, const int* __restrict__ hist, int* __restrict__ sorted,
+                                                        F8Lists lists) {
+    __shared__ int cnt[4096];
     __shared__ int tmp[48];
     const int t = threadIdx.x;
-    int c[4], first[4] = {};
+    int id[kF8Each];
+    f8_count(ids, P, E, !hist, cnt, id);
+    int all[4] = {}, before[4] = {}, start[4] = {};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int e = 4 * t + k;
-        c[k] = 0;
-        if (e >= E) continue;
-        if (given) {  // clamped: malformed offsets never address rows outside A or D
-            first[k] = min(max(given[e], 0), (int)P);
-            c[k] = min(max(given[e + 1], first[k]), (int)P) - first[k];
-        } else {
-            for (int i = 0; i < C; ++i) {
-                const int n = hist[(int64_t)i * E + e];
-                hist[(int64_t)i * E + e] = c[k];
-                c[k] += n;
+        if (!hist) all[k] = cnt[e];
+        else if (e < E)
+            for (int c = 0; c < (int)gridDim.x; ++c) {
+                const int n = hist[(int64_t)c * E + e];
+                all[k] += n;
+                before[k] += c < (int)blockIdx.x ? n : 0;
             }
-        }
     }
-    offsets_and_tiles(c, first, given != nullptr, E, given ? nullptr : off, lists, tmp);
+    offsets_and_tiles(all, start, false, blockIdx.x == 0, E, lists, tmp);  // (barriers inside: cnt is read)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) cnt[4 * t + k] = start[k] + before[k];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kF8Each; ++i)
+        if (id[i] >= 0) sorted[atomicAdd(&cnt[id[i]], 1)] = (int)((int64_t)blockIdx.x * kF8Chunk + i * 1024 + t);
 }
-// ... and the placing.
-__global__ __launch_bounds__(256) void f8_place_kernel(const int* __restrict__ ids, int64_t P, int E, const int* __restrict__ hist,
-                                                       const int* __restrict__ off, const int* __restrict__ rank, int* __restrict__ sorted) {
-    const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (p >= P) return;
-    const int v = ids[p];
-    if (v >= 0 && v < E) sorted[off[v] + hist[p / kF8Chunk * E + v] + rank[p]] = (int)p;
+// Grouped: the lists alone, from the offsets given.
+__global__ __launch_bounds__(1024) void f8_list_kernel(const int* __restrict__ given, int64_t P, int E, F8Lists lists) {
+    __shared__ int tmp[48];
+    int c[4] = {}, first[4] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int e = 4 * (int)threadIdx.x + k;
+        if (e >= E) continue;
+        // clamped: malformed offsets never address rows outside A or D
+        first[k] = min(max(given[e], 0), (int)P);
+        c[k] = min(max(given[e + 1], first[k]), (int)P) - first[k];
+    }
+    offsets_and_tiles(c, first, true, true, E, lists, tmp);
 }
 
 // ---------------------------------------------------------------------------
@@ -243,6 +236,7 @@ struct F8Params {
     int top_k;
     const Tile* tiles;
     const int* ntiles;
+    int max_tiles;      // entries of `tiles`
     const int* sorted;  // Indexed: pair of each sorted row
     // at most kF8InlineP pairs: the tile from the ids (Indexed) or offsets (Grouped)
     const int *ids, *offsets;
@@ -454,13 +448,20 @@ __global__ __launch_bounds__(256) void f8_stream_kernel(F8Params p) {
 constexpr int kF8Group = 6;
 constexpr int kF8Half = 128 * 128;  // bytes of A1 or A2 of a stage: 128 rows of a block
 
+// The row of A of local row r (past the tile's last: that one), and its row of D (past it: -1).
+__device__ __forceinline__ int f8_row(const F8Params& p, const Tile& tile, int r, int* d) {
+    const int pos = tile.first + min(r, tile.rows - 1), pair = p.sorted ? p.sorted[pos] : pos;
+    if (d) *d = r < tile.rows ? pair : -1;
+    return p.sorted ? pair / p.top_k : pos;
+}
+
 struct F8Stage {
     char *a1[2], *a2[2], *b[2];
     float* sa;
 };
 
 template <int MT>
-__device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int tn, const int* rowA, const int* rowD, const F8Stage& st) {
+__device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int tn, int* rowD, const F8Stage& st) {
     constexpr int NT = 4, H = MT >= 6 ? 4 : 2;                       // strips of a wave; subtiles of A1
     constexpr int L1 = H / 2, L2 = (MT - H + 1) / 2, LB = 4;         // loads of a block: 64 rows each, 8 KB each
     constexpr int kSa = kF8TileRows * 4;
@@ -471,17 +472,21 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int
     const rsrc_t rA = make_rsrc(p.A, (uint32_t)(p.a_rows * p.K));
     const rsrc_t rS = make_rsrc(p.S + (int64_t)tile.expert * p.s_estride, (uint32_t)(p.s_estride * 4));
     const rsrc_t rSA = make_rsrc(p.sa, (uint32_t)(p.a_rows * nb * 4));
+    // wave w loads the strips 2 w and 2 w + 1 (past the last: zeros, they lie behind the resource)
+    const uint32_t strip_bytes = (uint32_t)nb * 2048u, strip0 = (uint32_t)(tn * 16 + wave * 2) * strip_bytes, boff = (uint32_t)lane * 16u;
+#pragma unroll
+    for (int n = 0; n < LB; ++n)  // (block 0's weights: they need no row)
+        dma16(rW, (lds_char*)st.b[0] + wave * 4096 + n * 1024, boff, strip0 + (n >> 1) * strip_bytes + (n & 1) * 1024u);
     // 16-byte slot i * 512 + tid of A1 and A2 together: row slot / 8, and of it the unit
     // slot % 8 ^ (row >> 1 & 7), which spreads the reads of 16 rows over the banks
     uint32_t aoff[L1 + L2];
 #pragma unroll
     for (int i = 0; i < L1 + L2; ++i) {
         const int row = i * 64 + (tid >> 3), unit = (tid & 7) ^ ((row >> 1) & 7);
-        aoff[i] = (uint32_t)rowA[min(row, kF8TileRows - 1)] * (uint32_t)p.K + (uint32_t)unit * 16u;
+        aoff[i] = (uint32_t)f8_row(p, tile, row, nullptr) * (uint32_t)p.K + (uint32_t)unit * 16u;
     }
-    // wave w loads the strips 2 w and 2 w + 1 (past the last: zeros, they lie behind the resource)
-    const uint32_t strip_bytes = (uint32_t)nb * 2048u, strip0 = (uint32_t)(tn * 16 + wave * 2) * strip_bytes, boff = (uint32_t)lane * 16u;
-    const uint32_t saoff = (uint32_t)rowA[min(tid, kF8TileRows - 1)] * (uint32_t)nb * 4u;
+    uint32_t saoff = 0;
+    if (tid < kF8TileRows) saoff = (uint32_t)f8_row(p, tile, tid, rowD + tid) * (uint32_t)nb * 4u;
     // load n of the L1 + LB that M asks for (weights first), or of P's L2; past K the last
     // block again, not used
     auto load_m = [&](int blk, int s, int n) {
@@ -574,7 +579,7 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int
     using S2 = std::integral_constant<int, 2>;
     using S3 = std::integral_constant<int, 3>;
 #pragma unroll
-    for (int n = 0; n < L1 + LB; ++n) load_m(0, 0, n);
+    for (int n = LB; n < L1 + LB; ++n) load_m(0, 0, n);
 #pragma unroll
     for (int n = 0; n < L2; ++n) load_p(0, 0, n);
 #pragma unroll
@@ -635,39 +640,33 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     // touch what is read from another)
     __shared__ __attribute__((aligned(1024))) char a10[kF8Half], a11[kF8Half], a20[kF8Half], a21[kF8Half], b0[2 * kF8Half], b1[2 * kF8Half];
     __shared__ __attribute__((aligned(16))) float sas[2 * kF8TileRows * 4];
-    __shared__ int rowA[kF8TileRows], rowD[kF8TileRows];
+    __shared__ int rowD[kF8TileRows];
     const F8Stage st{{a10, a11}, {a20, a21}, {b0, b1}, sas};
     // Workgroups go round the 8 XCDs: neighbouring tiles to one of them.  Some 32 run on an
     // XCD at a time, and what they read in common comes into its L2 once: so up to kF8Group
     // m-tiles of one expert run side by side, for one 256 columns after the other
-    const int tiles_n = (p.N + 255) / 256, total = p.ntiles[1] * tiles_n;
-    int id = blockIdx.x;
-    if (id >= total) return;
-    id = (id & 7) * (total >> 3) + min(id & 7, total & 7) + (id >> 3);
+    // (256 workgroups at a time, 32 for each XCD: which tile is whose does not wait for how many there are)
+    const int tiles_n = (p.N + 255) / 256;
+    const int id = (blockIdx.x & ~255) + (blockIdx.x & 7) * 32 + ((blockIdx.x >> 3) & 31);
+    if (id / tiles_n >= p.max_tiles) return;
+    const int ntiles = p.ntiles[1];
     Tile tile = p.tiles[id / tiles_n];  // a tile of the same group
+    if (id / tiles_n >= ntiles) return;
     tile.expert = __builtin_amdgcn_readfirstlane(tile.expert);
     const int count = __builtin_amdgcn_readfirstlane(tile.rows), step = f8_tile_rows(count), number = __builtin_amdgcn_readfirstlane(tile.number);
     const int group = number / kF8Group * kF8Group, n = min(kF8Group, f8_tiles(count, 1) - group);
     const int in_group = id - (id / tiles_n - (number - group)) * tiles_n, tn = in_group / n, m = group + in_group % n;
     tile.first += m * step;
     tile.rows = min(step, count - m * step);
-    const int tid = threadIdx.x;
-    if (tid < kF8TileRows) {
-        const int pos = tile.first + min(tid, tile.rows - 1);
-        const int pair = p.sorted ? p.sorted[pos] : pos;
-        rowA[tid] = p.sorted ? pair / p.top_k : pos;
-        rowD[tid] = tid < tile.rows ? pair : -1;
-    }
-    __syncthreads();
     switch ((tile.rows + 31) / 32) {
         case 1:
         case 2:
-        case 3: return f8_tile<3>(p, tile, tn, rowA, rowD, st);
-        case 4: return f8_tile<4>(p, tile, tn, rowA, rowD, st);
-        case 5: return f8_tile<5>(p, tile, tn, rowA, rowD, st);
-        case 6: return f8_tile<6>(p, tile, tn, rowA, rowD, st);
-        case 7: return f8_tile<7>(p, tile, tn, rowA, rowD, st);
-        default: return f8_tile<8>(p, tile, tn, rowA, rowD, st);
+        case 3: return f8_tile<3>(p, tile, tn, rowD, st);
+        case 4: return f8_tile<4>(p, tile, tn, rowD, st);
+        case 5: return f8_tile<5>(p, tile, tn, rowD, st);
+        case 6: return f8_tile<6>(p, tile, tn, rowD, st);
+        case 7: return f8_tile<7>(p, tile, tn, rowD, st);
+        default: return f8_tile<8>(p, tile, tn, rowD, st);
     }
 }
 
@@ -705,7 +704,6 @@ hipError_t moe_f8_launch(const MoeF8Args& a) {
         hipLaunchKernelGGL(f8_stream_kernel, dim3((unsigned)(L.max_tiles[0] * p.ncb)), dim3(256), 0, a.stream, p);
         return hipGetLastError();
     }
-    int* off = (int*)(ws + L.offsets);
     int* sorted = (int*)(ws + L.sorted);
     F8Lists lists{};
     for (int i = 0; i < 2; ++i) {
@@ -713,26 +711,24 @@ hipError_t moe_f8_launch(const MoeF8Args& a) {
         lists.max_tiles[i] = (int)L.max_tiles[i];
     }
     lists.ntiles = (int*)(ws + L.ntiles);
-    const int C = (int)ceil_div(P, kF8Chunk);
-    if (!a.indexed) {
-        hipLaunchKernelGGL(f8_scan_kernel, dim3(1), dim3(1024), 0, a.stream, (int*)nullptr, 0, a.offsets, P, a.E, (int*)nullptr, lists);
-    } else if (C == 1) {
-        hipLaunchKernelGGL(f8_route_kernel, dim3(1), dim3(1024), 0, a.stream, a.ids, (int)P, a.E, sorted, lists);
+    if (a.indexed) {
+        const unsigned C = (unsigned)ceil_div(P, kF8Chunk);
+        int* hist = C > 1 ? (int*)(ws + L.hist) : nullptr;
+        if (hist) {
+            hipLaunchKernelGGL(f8_hist_kernel, dim3(C), dim3(1024), 0, a.stream, a.ids, P, a.E, hist);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+        hipLaunchKernelGGL(f8_place_kernel, dim3(C), dim3(1024), 0, a.stream, a.ids, P, a.E, (const int*)hist, sorted, lists);
     } else {
-        int *hist = (int*)(ws + L.hist), *rank = (int*)(ws + L.rank);
-        hipLaunchKernelGGL(f8_hist_kernel, dim3((unsigned)C), dim3(1024), 0, a.stream, a.ids, P, a.E, hist, rank);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL(f8_scan_kernel, dim3(1), dim3(1024), 0, a.stream, hist, C, (const int*)nullptr, P, a.E, off, lists);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL(f8_place_kernel, dim3((unsigned)ceil_div(P, 256)), dim3(256), 0, a.stream, a.ids, P, a.E, (const int*)hist, (const int*)off,
-                           (const int*)rank, sorted);
+        hipLaunchKernelGGL(f8_list_kernel, dim3(1), dim3(1024), 0, a.stream, a.offsets, P, a.E, lists);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     p.ntiles = lists.ntiles;
     p.sorted = a.indexed ? sorted : nullptr;
     if (L.max_tiles[1] > 0) {
         p.tiles = lists.tiles[1];
-        hipLaunchKernelGGL(f8_tile_kernel, dim3((unsigned)(L.max_tiles[1] * ceil_div(a.N, 256))), dim3(512), 0, a.stream, p);
+        p.max_tiles = lists.max_tiles[1];
+        hipLaunchKernelGGL(f8_tile_kernel, dim3((unsigned)(ceil_div(L.max_tiles[1] * ceil_div(a.N, 256), 256) * 256)), dim3(512), 0, a.stream, p);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     p.tiles = lists.tiles[0];
