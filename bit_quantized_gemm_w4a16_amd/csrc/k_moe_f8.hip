@@ -626,12 +626,40 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int
     for (int j = NT - 2; j < NT; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[MT - 1][j][r] += part[j & 3][r] * sc;
-    wait_vmcnt<0>();  // no direct load is in flight when the workgroup ends
+    wait_vmcnt<0>();  // no direct load is in flight any more
+    if (p.N % 8 == 0) {
+        // through LDS, a subtile at a time and each wave for itself: a lane holds 4 columns of
+        // a row, and 8 lanes store the wave's 128 bytes of it in 16 each (stored from where
+        // they are, 32 bytes of a row at a time, D took 58 us of 897)
+        lds_sync();  // every wave is done with the stages
+        char* mine = st.b[0] + wave * 2304;
+        const int r8 = lane >> 3, n = tn * 256 + wn * 64 + (lane & 7) * 8;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int row = rowD[(2 * i + wm) * 16 + col];
+        for (int i = 0; i < MT; ++i) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) f8_store(p, row, tn * 256 + wn * 64 + j * 16 + quad * 4, v4f{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]});
+            for (int j = 0; j < NT; ++j)
+                *(uint2*)(mine + col * 144 + j * 32 + quad * 8) =
+                    make_uint2((uint32_t)f32_to_bf16_bits(acc[i][j][0]) | ((uint32_t)f32_to_bf16_bits(acc[i][j][1]) << 16),
+                               (uint32_t)f32_to_bf16_bits(acc[i][j][2]) | ((uint32_t)f32_to_bf16_bits(acc[i][j][3]) << 16));
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const v4u v = *(const v4u*)(mine + (h * 8 + r8) * 144 + (lane & 7) * 16);
+                const int row = rowD[(2 * i + wm) * 16 + h * 8 + r8];
+                if (row >= 0 && n < p.N) *(v4u*)(p.D + (int64_t)row * p.N + n) = v;
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int row = rowD[(2 * i + wm) * 16 + col];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                f8_store(p, row, tn * 256 + wn * 64 + j * 16 + quad * 4, v4f{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]});
+        }
     }
 }
 
