@@ -30,8 +30,15 @@ namespace {
 
 constexpr int kF8InlineP = 64;   // one pair per lane of a wave
 constexpr int kF8Chunk = 4096;   // pairs of one routing workgroup
-constexpr int kF8Rows = 64;      // an expert with at most so many rows is one m-tile of the weight stream
-constexpr int kF8TileRows = 256; // else m-tiles of at most so many, of 32 rows each way
+constexpr int kF8TileRows = 256; // rows of a large m-tile, at most
+constexpr int kF8Rows = 32;      // rows that the weight stream takes at a time
+// Which experts the weight stream takes: those of up to kF8Rows rows where experts have
+// up to kF8Mean rows in the mean, else none.  Two launches of which each has a part of the
+// experts end one after the other, so what suits the mean runs it all.  32 experts of
+// 4096 x 7168, stream / tiles (us): mean 4 147 / 172, 8 149 / 171, 16 159 / 171, and with
+// the stream for up to 16 rows against tiles alone: mean 24 191 / 173, 32 186 / 175; 256
+// experts of 7168 x 2048: mean 8 611 / 624, 16 662 / 642, 31 703 / 668.
+constexpr int64_t kF8Mean = 16;
 constexpr int kF8Sa = 64;        // K blocks of activation scales in LDS at a time (weight stream)
 
 size_t al16(size_t b) { return (b + 15) / 16 * 16; }
@@ -45,9 +52,11 @@ struct Tile {
 
 struct F8Layout {  // byte offsets into the workspace
     size_t hist, sorted, tiles[2], ntiles, bytes;
+    int stream;            // as in F8Lists
     int64_t max_tiles[2];  // bounds of the lists of the weight stream's m-tiles and of the others
 };
 struct F8Lists {
+    int stream;  // experts of up to so many rows are for the weight stream (0: none)
     Tile* tiles[2];
     int* ntiles;  // [2]
     int max_tiles[2];
@@ -56,8 +65,10 @@ struct F8Lists {
 F8Layout f8_layout(int64_t T, int top_k, int E) {
     const int64_t P = T * top_k, C = ceil_div(P, kF8Chunk);
     F8Layout L{};
-    L.max_tiles[0] = E < P ? E : P;
-    const int64_t many = P / (kF8Rows + 1);  // experts that can have more rows
+    const int64_t held = E < P ? E : P;  // experts that can have a row
+    L.stream = P <= kF8InlineP || P <= kF8Mean * held ? kF8Rows : 0;
+    L.max_tiles[0] = L.stream ? held : 0;
+    const int64_t many = P / (L.stream + 1);  // experts that can have more rows
     L.max_tiles[1] = P / kF8TileRows + (E < many ? E : many);
     size_t o = 0;
     L.hist = o;
@@ -106,12 +117,12 @@ __device__ void scan3_1024(int (&v)[3], int* tmp) {
 
 // How many m-tiles an expert of c rows has in a list, and how many rows each (the last
 // may have fewer): the tiles of a large expert are as even as 32 rows allow.
-__device__ __forceinline__ int f8_tiles(int c, int list) {
-    return c == 0 || (c <= kF8Rows) != (list == 0) ? 0 : list == 0 ? 1 : (c + kF8TileRows - 1) / kF8TileRows;
+__device__ __forceinline__ int f8_tiles(int c, int list, int stream) {
+    return c == 0 || (c <= stream) != (list == 0) ? 0 : list == 0 ? 1 : (c + kF8TileRows - 1) / kF8TileRows;
 }
 __device__ __forceinline__ int f8_tile_rows(int c) {
     const int n = (c + kF8TileRows - 1) / kF8TileRows;
-    return c <= kF8Rows ? c : ((c + 31) / 32 + n - 1) / n * 32;
+    return ((c + 31) / 32 + n - 1) / n * 32;
 }
 
 // Where the experts' rows begin (in start), and the tile lists (where `list`), from the
@@ -122,8 +133,8 @@ __device__ void offsets_and_tiles(const int (&cnt)[4], int (&start)[4], bool giv
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         v[0] += cnt[k];
-        v[1] += f8_tiles(cnt[k], 0);
-        v[2] += f8_tiles(cnt[k], 1);
+        v[1] += f8_tiles(cnt[k], 0, lists.stream);
+        v[2] += f8_tiles(cnt[k], 1, lists.stream);
     }
     const int mine[2] = {v[1], v[2]};
     scan3_1024(v, tmp);
@@ -138,7 +149,7 @@ __device__ void offsets_and_tiles(const int (&cnt)[4], int (&start)[4], bool giv
             if (!given) start[k] = v[0];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int n = f8_tiles(cnt[k], i);
+                const int n = f8_tiles(cnt[k], i, lists.stream);
                 for (int q = 0; list && q < n && v[1 + i] + q < lists.max_tiles[i]; ++q)
                     lists.tiles[i][v[1 + i] + q] = Tile{e, start[k], cnt[k], q};
                 v[1 + i] += n;
@@ -298,7 +309,7 @@ __device__ __forceinline__ void f8_store(const F8Params& p, int row, int n, cons
 // hit the caches.  No barrier in the stream; scales of the rows sit in LDS.
 template <int MT>
 __device__ __forceinline__ void f8_stream(const F8Params& p, const Tile& tile, int cb, const int* rowA, const int* rowD, float* sal) {
-    constexpr int NT = 2, PF = MT == 4 ? 2 : 4;
+    constexpr int NT = 2, PF = 4;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, quad = lane >> 4;
     const int nb = p.nb;
@@ -372,7 +383,7 @@ __device__ __forceinline__ void f8_stream(const F8Params& p, const Tile& tile, i
 }
 
 __global__ __launch_bounds__(256) void f8_stream_kernel(F8Params p) {
-    __shared__ int rowA[kF8Rows], rowD[kF8Rows];
+    __shared__ int rowA[kF8InlineP], rowD[kF8InlineP];
     __shared__ __attribute__((aligned(16))) float sal[kF8SaRow * kF8Rows];
     __shared__ int owner[kF8InlineP];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -405,7 +416,7 @@ __global__ __launch_bounds__(256) void f8_stream_kernel(F8Params p) {
         const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(mine));
         const uint64_t rows = __ballot(id == e);
         tile = Tile{e, 0, (int)__popcll(rows), 0};
-        if (tid < kF8Rows) {
+        if (tid < kF8InlineP) {
             rowD[lane] = -1;
             rowA[lane] = p.ids ? __builtin_ctzll(rows) / p.top_k : __builtin_ctzll(rows);
             if (id == e) {
@@ -426,9 +437,11 @@ __global__ __launch_bounds__(256) void f8_stream_kernel(F8Params p) {
     tile.expert = __builtin_amdgcn_readfirstlane(tile.expert);
     tile.rows = __builtin_amdgcn_readfirstlane(tile.rows);
     __syncthreads();
-    if (tile.rows <= 16) f8_stream<1>(p, tile, cb, rowA, rowD, sal);
-    else if (tile.rows <= 32) f8_stream<2>(p, tile, cb, rowA, rowD, sal);
-    else f8_stream<4>(p, tile, cb, rowA, rowD, sal);
+    // (more than kF8Rows only where the pairs are so few that no list was made)
+    for (int r = 0; r < tile.rows; r += kF8Rows) {
+        if (tile.rows - r <= 16) f8_stream<1>(p, tile, cb, rowA + r, rowD + r, sal);
+        else f8_stream<2>(p, tile, cb, rowA + r, rowD + r, sal);
+    }
 }
 
 // ---- m-tiles of more rows: 256 x 256 of D on eight waves ----
@@ -682,7 +695,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     if (id / tiles_n >= ntiles) return;
     tile.expert = __builtin_amdgcn_readfirstlane(tile.expert);
     const int count = __builtin_amdgcn_readfirstlane(tile.rows), step = f8_tile_rows(count), number = __builtin_amdgcn_readfirstlane(tile.number);
-    const int group = number / kF8Group * kF8Group, n = min(kF8Group, f8_tiles(count, 1) - group);
+    const int group = number / kF8Group * kF8Group, n = min(kF8Group, (count + kF8TileRows - 1) / kF8TileRows - group);
     const int in_group = id - (id / tiles_n - (number - group)) * tiles_n, tn = in_group / n, m = group + in_group % n;
     tile.first += m * step;
     tile.rows = min(step, count - m * step);
@@ -734,6 +747,7 @@ hipError_t moe_f8_launch(const MoeF8Args& a) {
     }
     int* sorted = (int*)(ws + L.sorted);
     F8Lists lists{};
+    lists.stream = L.stream;
     for (int i = 0; i < 2; ++i) {
         lists.tiles[i] = (Tile*)(ws + L.tiles[i]);
         lists.max_tiles[i] = (int)L.max_tiles[i];
@@ -759,6 +773,7 @@ hipError_t moe_f8_launch(const MoeF8Args& a) {
         hipLaunchKernelGGL(f8_tile_kernel, dim3((unsigned)(ceil_div(L.max_tiles[1] * ceil_div(a.N, 256), 256) * 256)), dim3(512), 0, a.stream, p);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
+    if (L.max_tiles[0] == 0) return hipSuccess;
     p.tiles = lists.tiles[0];
     hipLaunchKernelGGL(f8_stream_kernel, dim3((unsigned)(L.max_tiles[0] * p.ncb)), dim3(256), 0, a.stream, p);
     return hipGetLastError();
