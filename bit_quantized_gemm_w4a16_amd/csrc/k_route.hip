@@ -5,11 +5,16 @@
 // themselves, which order the experts alike), the best groups by the sum of their
 // best members, the k best experts of those, and their weights.
 //
-// One wave per token, expert e = 64 i + lane of the wave.  Ranking values are
-// doubles: two experts whose fp32 scores round to the same value still come in
-// the order that the formula gives (a choice is a whole number, and a rounding
-// must not turn it).  v_max_f64 runs at the rate of v_max_f32 here.
+// One wave per token; lane l holds the NE experts from NE l on.  Scores and ranking
+// values are doubles: two experts whose fp32 scores round to the same value still come
+// in the order that the formula gives (a choice is a whole number, and a rounding must
+// not turn it); fp64 runs at the rate of fp32 here.  Bound by instructions: some 400 for
+// a token of 256 experts in 8 groups.  So the k best are not taken one after the other
+// (a reduction over the wave each) but by a threshold: the scalar unit searches bit by
+// bit for one that k lanes' best values reach, which lets in little more than k experts;
+// these move to a lane each and are ranked by counting.
 #include "hq_device.hpp"
+#include "hq_kv.h"
 #include "hq_layer.h"
 
 namespace hq {
@@ -23,165 +28,330 @@ struct RouteParams {
     float* weights;
     int64_t T, stride;
     int E, k, groups, top_groups, group_best;
-    int dtype, sigmoid, renorm;
+    FastDiv per_group;  // experts of a group
+    int in_lanes;       // lanes that hold a group, where it fills whole lanes, 1 2 4 8 or 16 of them (else 0)
+    int dtype, sigmoid, renorm, wide;
     float scale;
 };
 
 constexpr double kLowest = -__builtin_huge_val();
 
-__device__ __forceinline__ double shfl_xor_d(double v, int m) { return __shfl_xor(v, m); }
-
-// The order-preserving key of x as an unsigned: NaN is the lowest, -0 equals 0.
-// (Infinities keep their places: a bias of -inf ranks behind every number.)
-__device__ __forceinline__ double rank_of(double x) { return x != x ? kLowest : x; }
-
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) v = fmax(v, shfl_xor_d(v, m));
-    return v;
+// The value of lane `ctrl` says (DPP: no LDS), for reductions; every lane has a source.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
 }
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)u) | ((uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32));
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;  // (a mirror is a xor once its halves agree)
+
+__device__ __forceinline__ double from_lane(double v, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+// Over the wave, in every lane: within 16 lanes by DPP, the four rows' results by readlane.
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) v += shfl_xor_d(v, m);
-    return v;
+    v += dpp<kXor1>(v);
+    v += dpp<kXor2>(v);
+    v += dpp<kMirror8>(v);
+    v += dpp<kMirror16>(v);
+    return (from_lane(v, 0) + from_lane(v, 16)) + (from_lane(v, 32) + from_lane(v, 48));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    v = fmaxf(v, dpp<kXor1>(v));
+    v = fmaxf(v, dpp<kXor2>(v));
+    v = fmaxf(v, dpp<kMirror8>(v));
+    v = fmaxf(v, dpp<kMirror16>(v));
+    auto row = [&](int l) { return __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(v), l)); };
+    return fmaxf(fmaxf(row(0), row(16)), fmaxf(row(32), row(48)));
+}
+
+// e^x for x <= 0 (NaN: NaN): x = n ln 2 + r, the Taylor series of e^r to r^12 (|r| <= 0.347:
+// the rest is below 2^-52), scaled by 2^n; 20 instructions.
+__device__ __forceinline__ double exp_neg(double x) {
+    x = x < -1100.0 ? -1100.0 : x;
+    const double n = rint(x * 1.4426950408889634);
+    const double r = fma(-n, 1.9082149292705877e-10, fma(-n, 0.69314718036912382, x));  // ln 2 in two parts
+    double p = 1.0 / 479001600;
+    p = fma(p, r, 1.0 / 39916800);
+    p = fma(p, r, 1.0 / 3628800);
+    p = fma(p, r, 1.0 / 362880);
+    p = fma(p, r, 1.0 / 40320);
+    p = fma(p, r, 1.0 / 5040);
+    p = fma(p, r, 1.0 / 720);
+    p = fma(p, r, 1.0 / 120);
+    p = fma(p, r, 1.0 / 24);
+    p = fma(p, r, 1.0 / 6);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return ldexp(p, (int)n);
+}
+// 1 / (1 + e^-x): from t = e^-|x| <= 1, so without overflow; 1 / (1 + t) by two steps of
+// Newton's iteration.
+__device__ __forceinline__ double sigmoid(double x) {
+    const double t = exp_neg(-fabs(x)), d = 1.0 + t;
+    double y = __builtin_amdgcn_rcp(d);
+    y = fma(fma(-d, y, 1.0), y, y);
+    y = fma(fma(-d, y, 1.0), y, y);
+    return x < 0 ? t * y : y;
+}
+
+// NaN ranks with -inf.
+__device__ __forceinline__ double rank_of(double x) { return x != x ? kLowest : x; }
+// Unsigned integers in the order of the values (-0 as 0); every value's is above 0.
+__device__ __forceinline__ uint64_t ordered(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x + 0.0);
+    return u ^ (uint64_t)((int64_t)u >> 63 | (int64_t)0x8000000000000000ull);
+}
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u ^ (uint32_t)((int32_t)u >> 31 | (int32_t)0x80000000);
 }
 
 template <int NE>
 __global__ __launch_bounds__(256) void route_kernel(RouteParams p) {
-    extern __shared__ double members[];  // [4 waves][E], with groups
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    extern __shared__ double members[];         // [4 waves][E], for groups that do not fill whole lanes
+    __shared__ uint32_t picked[4][3][64];       // each wave's few: the two halves of the key, the expert
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t = (int64_t)blockIdx.x * 4 + wave;
     if (t >= p.T) return;  // whole waves; no barrier below
-    const int E = p.E;
+    const int E = p.E, e0 = lane * NE;
 
+    auto logit = [&](int e) {
+        const int64_t at = t * p.stride + e;
+        return p.dtype == HQ_DT_FP32   ? ((const float*)p.logits)[at]
+               : p.dtype == HQ_DT_BF16 ? bits16_to_f32<true>(((const uint16_t*)p.logits)[at])
+                                       : bits16_to_f32<false>(((const uint16_t*)p.logits)[at]);
+    };
     float l[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const int e = 64 * i + lane;
-        l[i] = -INFINITY;
-        if (e < E) {
-            const int64_t at = t * p.stride + e;
-            l[i] = p.dtype == HQ_DT_FP32   ? ((const float*)p.logits)[at]
-                   : p.dtype == HQ_DT_BF16 ? bits16_to_f32<true>(((const uint16_t*)p.logits)[at])
-                                           : bits16_to_f32<false>(((const uint16_t*)p.logits)[at]);
-        }
-    }
-    // scores: sigmoid from e^-|l| <= 1; softmax less the largest logit
-    double s[NE];
-    if (p.sigmoid) {
+    for (int i = 0; i < NE; ++i) l[i] = -INFINITY;
+    if (NE % 4 == 0 && p.wide && e0 < E) {  // fp32 rows of whole 16 bytes
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const double x = l[i], e = exp(-fabs(x));
-            s[i] = (x >= 0 ? 1.0 : e) / (1.0 + e);
+        for (int i = 0; i < NE / 4; ++i) {
+            if (e0 + 4 * i >= E) break;
+            const v4f v = *(const v4f*)((const float*)p.logits + t * p.stride + e0 + 4 * i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) l[(4 * i + j) % NE] = v[j];
         }
     } else {
-        float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) m = fmaxf(m, l[i]);
+        for (int i = 0; i < NE; ++i)
+            if (e0 + i < E) l[i] = logit(e0 + i);
+    }
+    float top = 0.f;  // the largest logit (softmax)
+    if (!p.sigmoid) {
+        top = l[0];
 #pragma unroll
-        for (int x = 32; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
+        for (int i = 1; i < NE; ++i) top = fmaxf(top, l[i]);
+        top = wave_max(top);
+    }
+    auto score = [&](float x) {
+        if (p.sigmoid) return sigmoid((double)x);
+        return top == -INFINITY && x == top ? 0.0 : exp_neg((double)x - (double)top);
+    };
+    // Every expert's score: only where it ranks, or counts in a sum.  (Where the weights are
+    // renormalised and nothing else asks, the sum over all experts cancels.)
+    const bool pairs = p.groups > 1 && p.group_best == 2;
+    double s[NE], inv = 1.0;
+    if (p.bias || pairs || (!p.sigmoid && !p.renorm)) {
         double sum = 0;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            s[i] = m == -INFINITY && l[i] == m ? 0.0 : exp((double)l[i] - (double)m);
-            sum += s[i];
+            s[i] = score(l[i]);
+            sum += e0 + i < E ? s[i] : 0.0;
         }
-        sum = wave_sum(sum);
-        const double inv = sum == 0 ? 0.0 : 1.0 / sum;  // (every logit -inf: weights 0)
+        if (!p.sigmoid) {
+            sum = wave_sum(sum);
+            inv = sum == 0 ? 0.0 : 1.0 / sum;  // (every logit -inf: weights 0)
 #pragma unroll
-        for (int i = 0; i < NE; ++i) s[i] *= inv;
+            for (int i = 0; i < NE; ++i) s[i] *= inv;
+        }
     }
+    if (!p.sigmoid) {  // a NaN among the logits is in every weight
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) nan = nan || l[i] != l[i];
+        if (__ballot(nan)) inv = __builtin_nan("");
+    }
+    // keys: unsigned integers in the order of the ranking, 0 for what cannot be taken
+    uint32_t hi[NE], lo[NE];
     double c[NE];
-    uint64_t open = 0;  // bit i: expert 64 i + lane may still be taken
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-        const int e = 64 * i + lane;
-        c[i] = p.bias ? s[i] + (double)(e < E ? p.bias[e] : 0.f) : (double)l[i];
-        c[i] = rank_of(c[i]);
-        if (e < E) open |= 1ull << i;
+        const int e = e0 + i;
+        lo[i] = 0;
+        if (p.bias) {
+            c[i] = rank_of(s[i] + (double)(e < E ? p.bias[e] : 0.f));
+            const uint64_t k = ordered(c[i]);
+            hi[i] = (uint32_t)(k >> 32);
+            lo[i] = (uint32_t)k;
+        } else {
+            c[i] = pairs ? rank_of(s[i]) : rank_of((double)l[i]);
+            hi[i] = ordered(l[i] != l[i] ? -INFINITY : l[i]);
+        }
+        if (e >= E) hi[i] = 0;
     }
 
     if (p.groups > 1) {
-        // the value of a group: the sum of its best one or two ranking values (scores,
-        // where there is no bias).  64 / L groups at a time, L lanes to a group.
-        const int S = E / p.groups;
-        double* mine = members + (int64_t)wave * E;
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (64 * i + lane < E) mine[64 * i + lane] = p.bias ? c[i] : rank_of(s[i]);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        int L = 64;
-        while (L > 1 && L * p.groups > 64) L >>= 1;
-        const int g = lane / L;
+        // the value of a group: the sum of its best one or two; L lanes to a group
+        const int S = (int)p.per_group.d;
+        int L = p.in_lanes;
         double a = kLowest, b = kLowest;  // the two best, a >= b
-        if (g < p.groups)
-            for (int i = lane % L; i < S; i += L) {
-                const double v = mine[g * S + i];
-                b = fmax(b, fmin(a, v));
-                a = fmax(a, v);
-            }
-        for (int x = 1; x < L; x <<= 1) {
-            const double a2 = shfl_xor_d(a, x), b2 = shfl_xor_d(b, x);
+        auto take = [&](double v) {
+            b = fmax(b, fmin(a, v));
+            a = fmax(a, v);
+        };
+        if (L) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i)
+                if (e0 + i < E) take(c[i]);
+        } else {
+            double* mine = members + (int64_t)wave * E;
+#pragma unroll
+            for (int i = 0; i < NE; ++i)
+                if (e0 + i < E) mine[e0 + i] = c[i];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            L = 64;
+            while (L > 1 && L * p.groups > 64) L >>= 1;
+            const int g = lane / L;
+            if (g < p.groups)
+                for (int i = lane % L; i < S; i += L) take(mine[g * S + i]);
+        }
+        auto join = [&](double a2, double b2) {
             b = fmax(fmin(a, a2), fmax(b, b2));
             a = fmax(a, a2);
-        }
+        };
+        if (L > 1) join(dpp<kXor1>(a), dpp<kXor1>(b));
+        if (L > 2) join(dpp<kXor2>(a), dpp<kXor2>(b));
+        if (L > 4) join(dpp<kMirror8>(a), dpp<kMirror8>(b));
+        if (L > 8) join(dpp<kMirror16>(a), dpp<kMirror16>(b));
+        for (int x = 16; x < L; x <<= 1) join(__shfl_xor(a, x), __shfl_xor(b, x));
         const double value = p.group_best == 2 ? rank_of(a + b) : a;
         // groups that stay: fewer than top_groups are better (the lower of equals is)
+        const int g = lane / L;
         int better = 0;
         for (int o = 0; o < p.groups; ++o) {
-            const double v = __shfl(value, o * L);
+            const double v = from_lane(value, o * L);
             better += v > value || (v == value && o < g) ? 1 : 0;
         }
-        const uint64_t stay = __ballot(better < p.top_groups && g < p.groups);
+        const bool stays = better < p.top_groups && g < p.groups;
+        if (p.in_lanes) {
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int e = 64 * i + lane;
-            if (e < E && !((stay >> (e / S * L)) & 1)) open &= ~(1ull << i);
+            for (int i = 0; i < NE; ++i) hi[i] = stays ? hi[i] : 0;
+        } else {
+            const uint64_t stay = __ballot(stays);
+#pragma unroll
+            for (int i = 0; i < NE; ++i)
+                if (e0 + i < E && !((stay >> (p.per_group.div(e0 + i) * L)) & 1)) hi[i] = 0;
         }
     }
 
-    // the k best: of the lanes' best values the largest, the lowest expert of equals
-    int32_t* ids = p.ids + t * p.k;
-    int my_id = 0;
-    double my_s = 0, total = 0;
-    for (int r = 0; r < p.k; ++r) {
-        double best = kLowest;
-        int at = 1 << 20;  // the lane's lowest open expert with that value
+    // a threshold that at least k lanes' best keys reach, and few more (fewer than k lanes: 0)
+    uint32_t best = hi[0];
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const bool is = ((open >> i) & 1) && (c[i] > best || at == 1 << 20);
-            best = is ? c[i] : best;
-            at = is ? 64 * i + lane : at;
-        }
-        const double top = wave_max(best);
-        int win = best == top ? at : 1 << 20;
-#pragma unroll
-        for (int x = 32; x > 0; x >>= 1) win = min(win, __shfl_xor(win, x));
-        // (an open expert is always left: k is at most the experts of the groups that stay)
-        double score = 0;
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (i == win / 64) score = s[i];
-        score = __shfl(score, win & 63);
-        if ((win & 63) == lane) open &= ~(1ull << (win >> 6));
-        total += score;
-        if (lane == r) {
-            my_id = win;
-            my_s = score;
+    for (int i = 1; i < NE; ++i) best = max(best, hi[i]);
+    uint32_t bar = 0;
+    for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
+        const int n = __popcll(__ballot(best >= (bar | bit)));
+        if (n >= p.k) {
+            bar |= bit;
+            if (n <= p.k + 2) break;
         }
     }
+    bar = max(bar, 1u);
+    int before = 0, total = 0;  // picked experts of the lanes before, of all
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const uint64_t m = __ballot(hi[i] >= bar);
+        before += __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+        total += __popcll(m);
+    }
+    int32_t* ids = p.ids + t * p.k;
+    float* weights = p.weights + t * p.k;
+    if (total <= 64) {
+        // a lane each, in the experts' order
+        uint32_t(*mine)[64] = picked[wave];
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            if (hi[i] >= bar) {
+                mine[0][before] = hi[i];
+                mine[1][before] = lo[i];
+                mine[2][before] = (uint32_t)(e0 + i);
+                ++before;
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const uint64_t key = (uint64_t)mine[0][lane] << 32 | mine[1][lane];
+        const int e = lane < total ? (int)mine[2][lane] : 0;
+        const float x = lane < total ? logit(e) : 0.f;
+        int rank = 0;
+        for (int j = 0; j < total; ++j) {
+            const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(key >> 32), j) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, j);
+            rank += o > key || (o == key && j < lane) ? 1 : 0;
+        }
+        const bool chosen = lane < total && rank < p.k;
+        double w = chosen ? score(x) * inv : 0.0;
+        if (p.renorm) {
+            const double sum = wave_sum(w);
+            w = sum == 0 ? 0.0 : w / sum;
+        }
+        if (chosen) {
+            ids[rank] = e;
+            weights[rank] = (float)(w * (double)p.scale);
+        }
+        return;
+    }
+    // More than a lane each (many equal keys, or k near the number of lanes): one after the
+    // other, the lowest expert of equals
+    int my_id = 0;
+    for (int r = 0; r < p.k; ++r) {
+        uint64_t mine = 0;
+        int at = 1 << 20;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const uint64_t k = (uint64_t)hi[i] << 32 | lo[i];
+            const bool is = hi[i] && k > mine;
+            mine = is ? k : mine;
+            at = is ? e0 + i : at;
+        }
+        uint64_t most = mine;
+        for (int x = 32; x > 0; x >>= 1) {
+            const uint64_t o = __shfl_xor((unsigned long long)most, x);
+            most = o > most ? o : most;
+        }
+        const int win = __builtin_amdgcn_readlane(at, __builtin_ctzll(__ballot(mine == most)));  // (lanes hold experts in order)
+#pragma unroll
+        for (int i = 0; i < NE; ++i) hi[i] = e0 + i == win ? 0 : hi[i];
+        if (lane == r) my_id = win;
+    }
+    double w = lane < p.k ? score(logit(my_id)) * inv : 0.0;
+    if (p.renorm) {
+        const double sum = wave_sum(w);
+        w = sum == 0 ? 0.0 : w / sum;
+    }
     if (lane < p.k) {
-        double w = my_s;
-        if (p.renorm) w = total == 0 ? 0.0 : w / total;
         ids[lane] = my_id;
-        p.weights[t * p.k + lane] = (float)(w * (double)p.scale);
+        weights[lane] = (float)(w * (double)p.scale);
     }
 }
 
 template <int NE>
-hipError_t go(const RouteParams& p, hipStream_t st) {
-    const size_t lds = p.groups > 1 ? (size_t)p.E * 4 * sizeof(double) : 0;
+hipError_t go(RouteParams p, hipStream_t st) {
+    const int S = p.E / p.groups, lanes = S / NE;
+    p.in_lanes = S % NE == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    const size_t lds = p.groups > 1 && !p.in_lanes ? (size_t)p.E * 4 * sizeof(double) : 0;
     static const hipError_t attr = hipFuncSetAttribute((const void*)route_kernel<NE>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                                        64 * NE * 4 * (int)sizeof(double));
     if (attr != hipSuccess) return attr;
@@ -281,6 +451,8 @@ hipError_t route_launch(const RouteArgs& a) {
     p.groups = a.groups;
     p.top_groups = a.top_groups;
     p.group_best = a.group_best;
+    p.per_group = FastDiv::of((uint32_t)(a.experts / a.groups));
+    p.wide = a.dtype == HQ_DT_FP32 && a.stride % 4 == 0 && a.experts % 4 == 0;
     p.dtype = a.dtype;
     p.sigmoid = a.sigmoid;
     p.renorm = a.renorm;
