@@ -5,14 +5,16 @@
 // themselves, which order the experts alike), the best groups by the sum of their
 // best members, the k best experts of those, and their weights.
 //
-// One wave per token; lane l holds the NE experts from NE l on.  Scores and ranking
-// values are doubles: two experts whose fp32 scores round to the same value still come
-// in the order that the formula gives (a choice is a whole number, and a rounding must
-// not turn it); fp64 runs at the rate of fp32 here.  Bound by instructions: some 400 for
-// a token of 256 experts in 8 groups.  So the k best are not taken one after the other
-// (a reduction over the wave each) but by a threshold: the scalar unit searches bit by
-// bit for one that k lanes' best values reach, which lets in little more than k experts;
-// these move to a lane each and are ranked by counting.
+// A choice is a whole number, and a rounding must not turn it: two experts whose fp32
+// scores round to the same value still come in the order that the formula gives.  Doubles
+// for every expert would do, and cost twice the instructions, which are what bounds the
+// kernel (one wave per token, lane l holding the NE experts from NE l on).  So fp32
+// values, whose errors have a bound, only rule out: a threshold is searched bit by bit on
+// the scalar unit that k lanes' best values reach (the k best taken one after the other
+// would be a reduction over the wave each); what lies below it by more than the bound is
+// out, and the few others, little more than k, move to a lane each, get their value in
+// 64 bits and are ranked by counting.  Groups whose order the bound leaves open are
+// formed in 64 bits; a NaN, or more than 64 left, sends a token to a slow way.
 #include "hq_device.hpp"
 #include "hq_kv.h"
 #include "hq_layer.h"
@@ -105,6 +107,13 @@ __device__ __forceinline__ double sigmoid(double x) {
     return x < 0 ? t * y : y;
 }
 
+// 1 / x for normal x (v_rcp_f64 and two steps of Newton's iteration).
+__device__ __forceinline__ double reciprocal(double x) {
+    double y = __builtin_amdgcn_rcp(x);
+    y = fma(fma(-x, y, 1.0), y, y);
+    return fma(fma(-x, y, 1.0), y, y);
+}
+
 // NaN ranks with -inf.
 __device__ __forceinline__ double rank_of(double x) { return x != x ? kLowest : x; }
 // Unsigned integers in the order of the values (-0 as 0); every value's is above 0.
@@ -116,25 +125,124 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t u = __float_as_uint(x + 0.0f);
     return u ^ (uint32_t)((int32_t)u >> 31 | (int32_t)0x80000000);
 }
+__device__ __forceinline__ float value_of(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
 
-template <int NE>
-__global__ __launch_bounds__(256) void route_kernel(RouteParams p) {
-    extern __shared__ double members[];         // [4 waves][E], for groups that do not fill whole lanes
-    __shared__ uint32_t picked[4][3][64];       // each wave's few: the two halves of the key, the expert
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-    if (t >= p.T) return;  // whole waves; no barrier below
-    const int E = p.E, e0 = lane * NE;
+// What the ways to choose have in common: a token's logits, its scores in 64 bits.
+struct Token {
+    const RouteParams& p;
+    int64_t t;
+    float top;     // the largest logit (softmax)
+    double inv;    // what scores are multiplied by: 1 / the sum over all experts, where it counts
 
-    auto logit = [&](int e) {
+    __device__ __forceinline__ float logit(int e) const {
         const int64_t at = t * p.stride + e;
         return p.dtype == HQ_DT_FP32   ? ((const float*)p.logits)[at]
                : p.dtype == HQ_DT_BF16 ? bits16_to_f32<true>(((const uint16_t*)p.logits)[at])
                                        : bits16_to_f32<false>(((const uint16_t*)p.logits)[at]);
-    };
-    float l[NE];
+    }
+    __device__ __forceinline__ double score(float x) const {  // not yet times inv
+        if (p.sigmoid) return sigmoid((double)x);
+        return top == -INFINITY && x == top ? 0.0 : exp_neg((double)x - (double)top);
+    }
+    // The weights of the chosen: lane `chosen` has score w (times inv) of expert e, rank r.
+    __device__ __forceinline__ void store(bool chosen, double w, int e, int r) const {
+        w = chosen ? w : 0.0;
+        if (p.renorm) {
+            const double sum = wave_sum(w);
+            w = sum == 0 ? 0.0 : sum > 1e-290 ? w * reciprocal(sum) : w / sum;
+        }
+        if (chosen) {
+            p.ids[t * p.k + r] = e;
+            p.weights[t * p.k + r] = (float)(w * (double)p.scale);
+        }
+    }
+};
+
+// What ranks expert e.
+__device__ __forceinline__ double rank_value(const Token& tok, int e) {
+    const float x = tok.logit(e);
+    return rank_of(tok.p.bias ? tok.score(x) * tok.inv + (double)tok.p.bias[e] : (double)x);
+}
+
+// Whether group lane / L stays, in 64 bits; L lanes to a group look at its members.
+__device__ __forceinline__ bool group_stays(const Token& tok, int L) {
+    const RouteParams& p = tok.p;
+    const int lane = threadIdx.x & 63, S = (int)p.per_group.d, g = lane / L;
+    double a = kLowest, b = kLowest;  // the two best, a >= b
+    if (g < p.groups)
+        for (int i = lane % L; i < S; i += L) {
+            const int e = g * S + i;
+            const double v = p.bias || p.group_best == 1 ? rank_value(tok, e) : rank_of(tok.score(tok.logit(e)) * tok.inv);
+            b = fmax(b, fmin(a, v));
+            a = fmax(a, v);
+        }
+    for (int x = 1; x < L; x <<= 1) {
+        const double a2 = __shfl_xor(a, x), b2 = __shfl_xor(b, x);
+        b = fmax(fmin(a, a2), fmax(b, b2));
+        a = fmax(a, a2);
+    }
+    const double value = p.group_best == 2 ? rank_of(a + b) : a;
+    int better = 0;  // fewer than top_groups are better than one that stays (of equals the lower is)
+    for (int o = 0; o < p.groups; ++o) {
+        const double v = from_lane(value, o * L);
+        better += v > value || (v == value && o < g) ? 1 : 0;
+    }
+    return better < p.top_groups && g < p.groups;
+}
+__device__ __forceinline__ int lanes_of_group(int groups) {
+    int L = 64;
+    while (L > 1 && L * groups > 64) L >>= 1;
+    return L;
+}
+
+// The slow way: everything in 64 bits, formed anew wherever it is looked at; the k best one
+// after the other.
+__device__ __forceinline__ void route_slowly(const Token& tok) {
+    const RouteParams& p = tok.p;
+    const int lane = threadIdx.x & 63, L = lanes_of_group(p.groups);
+    const uint64_t stay = p.groups > 1 ? __ballot(group_stays(tok, L)) : ~0ull;
+    uint64_t taken = 0;  // bit i: expert 64 i + lane
+    int my_id = 0;
+    for (int r = 0; r < p.k; ++r) {
+        double best = kLowest;
+        int at = 1 << 20;
+        for (int i = 0, e = lane; e < p.E; ++i, e += 64) {
+            if (((taken >> i) & 1) || (p.groups > 1 && !((stay >> (p.per_group.div(e) * L)) & 1))) continue;
+            const double v = rank_value(tok, e);
+            if (v > best || at == 1 << 20) {
+                best = v;
+                at = e;
+            }
+        }
+        // the largest, the lowest expert of equals (one is always left: k is at most the
+        // experts of the groups that stay)
+        for (int x = 32; x > 0; x >>= 1) {
+            const double v = __shfl_xor(best, x);
+            const int o = __shfl_xor(at, x);
+            const bool is = (o < 1 << 20) && (at == 1 << 20 || v > best || (v == best && o < at));
+            best = is ? v : best;
+            at = is ? o : at;
+        }
+        if (at % 64 == lane) taken |= 1ull << (at / 64);
+        if (lane == r) my_id = at;
+    }
+    tok.store(lane < p.k, lane < p.k ? tok.score(tok.logit(my_id)) * tok.inv : 0.0, my_id, lane);
+}
+
+// The quick way; false where it cannot tell.
+template <int NE>
+__device__ __forceinline__ bool route_quickly(const RouteParams& p, Token& tok, float* members, uint32_t* mine) {
+    const int lane = threadIdx.x & 63, E = p.E, e0 = lane * NE;
+    const int64_t t = tok.t;
+
+    float l[NE], bias[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) l[i] = -INFINITY;
+    for (int i = 0; i < NE; ++i) {
+        l[i] = -INFINITY;
+        bias[i] = 0.f;
+    }
     if (NE % 4 == 0 && p.wide && e0 < E) {  // fp32 rows of whole 16 bytes
 #pragma unroll
         for (int i = 0; i < NE / 4; ++i) {
@@ -142,125 +250,138 @@ __global__ __launch_bounds__(256) void route_kernel(RouteParams p) {
             const v4f v = *(const v4f*)((const float*)p.logits + t * p.stride + e0 + 4 * i);
 #pragma unroll
             for (int j = 0; j < 4; ++j) l[(4 * i + j) % NE] = v[j];
+            if (p.bias) {
+                const v4f b = *(const v4f*)(p.bias + e0 + 4 * i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) bias[(4 * i + j) % NE] = b[j];
+            }
         }
     } else {
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-            if (e0 + i < E) l[i] = logit(e0 + i);
+            if (e0 + i < E) {
+                l[i] = tok.logit(e0 + i);
+                if (p.bias) bias[i] = p.bias[e0 + i];
+            }
     }
-    float top = 0.f;  // the largest logit (softmax)
+    bool odd = false;  // a NaN among the logits
+#pragma unroll
+    for (int i = 0; i < NE; ++i) odd = odd || l[i] != l[i];
+    // Scores.  Softmax in 64 bits, where the sum over all experts counts (where the weights are
+    // renormalised and nothing else asks, it cancels).  Sigmoid: e^-|l| and 1 / (1 + e^-|l|)
+    // from the hardware's exp2 and reciprocal (each off by one unit of fp32, the argument
+    // by 2^-24 of itself, which t = e^-|l| makes less than 2^-24 again): within 2^-21.
+    const bool pairs = p.groups > 1 && p.group_best == 2, scored = p.bias || pairs;
+    float c[NE];  // ranking values
     if (!p.sigmoid) {
-        top = l[0];
+        float top = l[0];
 #pragma unroll
         for (int i = 1; i < NE; ++i) top = fmaxf(top, l[i]);
-        top = wave_max(top);
-    }
-    auto score = [&](float x) {
-        if (p.sigmoid) return sigmoid((double)x);
-        return top == -INFINITY && x == top ? 0.0 : exp_neg((double)x - (double)top);
-    };
-    // Every expert's score: only where it ranks, or counts in a sum.  (Where the weights are
-    // renormalised and nothing else asks, the sum over all experts cancels.)
-    const bool pairs = p.groups > 1 && p.group_best == 2;
-    double s[NE], inv = 1.0;
-    if (p.bias || pairs || (!p.sigmoid && !p.renorm)) {
-        double sum = 0;
+        tok.top = wave_max(top);
+        if (scored || !p.renorm) {
+            double s[NE], sum = 0;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                s[i] = tok.score(l[i]);
+                sum += e0 + i < E ? s[i] : 0.0;
+            }
+            sum = wave_sum(sum);
+            tok.inv = sum == 0 ? 0.0 : 1.0 / sum;  // (every logit -inf: weights 0)
+#pragma unroll
+            for (int i = 0; i < NE; ++i) c[i] = (float)(s[i] * tok.inv);
+        }
+        if (__ballot(odd)) tok.inv = __builtin_nan("");  // a NaN is in every weight
+    } else if (scored) {
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            s[i] = score(l[i]);
-            sum += e0 + i < E ? s[i] : 0.0;
-        }
-        if (!p.sigmoid) {
-            sum = wave_sum(sum);
-            inv = sum == 0 ? 0.0 : 1.0 / sum;  // (every logit -inf: weights 0)
-#pragma unroll
-            for (int i = 0; i < NE; ++i) s[i] *= inv;
+            const float x = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(l[i])), y = __builtin_amdgcn_rcpf(1.0f + x);
+            c[i] = l[i] < 0 ? x * y : y;
         }
     }
-    if (!p.sigmoid) {  // a NaN among the logits is in every weight
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < NE; ++i) nan = nan || l[i] != l[i];
-        if (__ballot(nan)) inv = __builtin_nan("");
-    }
-    // keys: unsigned integers in the order of the ranking, 0 for what cannot be taken
-    uint32_t hi[NE], lo[NE];
-    double c[NE];
+    // How far c may be off: scores by 2^-20, the sum with a bias by 2^-24 of itself.
+    auto off = [&](float v) { return p.bias ? 0x1p-19f + 0x1p-22f * fabsf(v) : 0.f; };
+    uint32_t key[NE];  // in the order of the ranking, 0 for what cannot be taken
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-        const int e = e0 + i;
-        lo[i] = 0;
-        if (p.bias) {
-            c[i] = rank_of(s[i] + (double)(e < E ? p.bias[e] : 0.f));
-            const uint64_t k = ordered(c[i]);
-            hi[i] = (uint32_t)(k >> 32);
-            lo[i] = (uint32_t)k;
-        } else {
-            c[i] = pairs ? rank_of(s[i]) : rank_of((double)l[i]);
-            hi[i] = ordered(l[i] != l[i] ? -INFINITY : l[i]);
-        }
-        if (e >= E) hi[i] = 0;
+        if (p.bias) c[i] += bias[i];
+        else if (!pairs) c[i] = l[i];
+        key[i] = e0 + i < E ? ordered(p.bias ? c[i] : l[i]) : 0;
     }
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) odd = odd || c[i] != c[i];
+    }
+    if (__ballot(odd)) return false;
 
     if (p.groups > 1) {
         // the value of a group: the sum of its best one or two; L lanes to a group
         const int S = (int)p.per_group.d;
         int L = p.in_lanes;
-        double a = kLowest, b = kLowest;  // the two best, a >= b
-        auto take = [&](double v) {
-            b = fmax(b, fmin(a, v));
-            a = fmax(a, v);
+        float a = -INFINITY, b = -INFINITY;  // the two best, a >= b
+        auto take = [&](float v) {
+            b = fmaxf(b, fminf(a, v));
+            a = fmaxf(a, v);
         };
         if (L) {
 #pragma unroll
             for (int i = 0; i < NE; ++i)
                 if (e0 + i < E) take(c[i]);
         } else {
-            double* mine = members + (int64_t)wave * E;
 #pragma unroll
             for (int i = 0; i < NE; ++i)
-                if (e0 + i < E) mine[e0 + i] = c[i];
+                if (e0 + i < E) members[e0 + i] = c[i];
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
-            L = 64;
-            while (L > 1 && L * p.groups > 64) L >>= 1;
+            L = lanes_of_group(p.groups);
             const int g = lane / L;
             if (g < p.groups)
-                for (int i = lane % L; i < S; i += L) take(mine[g * S + i]);
+                for (int i = lane % L; i < S; i += L) take(members[g * S + i]);
         }
-        auto join = [&](double a2, double b2) {
-            b = fmax(fmin(a, a2), fmax(b, b2));
-            a = fmax(a, a2);
+        auto join = [&](float a2, float b2) {
+            b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+            a = fmaxf(a, a2);
         };
         if (L > 1) join(dpp<kXor1>(a), dpp<kXor1>(b));
         if (L > 2) join(dpp<kXor2>(a), dpp<kXor2>(b));
         if (L > 4) join(dpp<kMirror8>(a), dpp<kMirror8>(b));
         if (L > 8) join(dpp<kMirror16>(a), dpp<kMirror16>(b));
         for (int x = 16; x < L; x <<= 1) join(__shfl_xor(a, x), __shfl_xor(b, x));
-        const double value = p.group_best == 2 ? rank_of(a + b) : a;
-        // groups that stay: fewer than top_groups are better (the lower of equals is)
-        const int g = lane / L;
-        int better = 0;
-        for (int o = 0; o < p.groups; ++o) {
-            const double v = from_lane(value, o * L);
-            better += v > value || (v == value && o < g) ? 1 : 0;
+        // A group stays where fewer than top_groups are better (of equals the lower is).  Values
+        // with errors: where it is sure whether so many are.  (The sum of two: both errors, and
+        // 2^-24 of the sum.)
+        const float value = pairs ? a + b : a;
+        const float err = scored ? 0x1p-17f + 0x1p-20f * (fabsf(a) + (pairs ? fabsf(b) : 0.f)) : 0.f;
+        const float low = value - err, high = value + err;
+        const int g = lane / L, x = lane % L;
+        int sure = 0, maybe = 0;
+        const uint64_t mask = L == 64 ? ~0ull : (1ull << L) - 1;
+        for (int o = 0; o < p.groups; o += L) {  // lane x of each group looks at group o + x
+            const int other = o + x;
+            const float low_o = __shfl(low, other * L), high_o = __shfl(high, other * L);
+            const bool is = other < p.groups && other != g;
+            const bool s = is && (low_o > high || (!scored && low_o == high && other < g));
+            const bool m = scored ? is && high_o >= low : s;
+            sure += __popcll(__ballot(s) >> (lane - x) & mask);
+            maybe += __popcll(__ballot(m) >> (lane - x) & mask);
         }
-        const bool stays = better < p.top_groups && g < p.groups;
+        bool stays = maybe < p.top_groups && g < p.groups;
+        const bool open = g < p.groups && ((!stays && sure < p.top_groups) || (scored && !(err < INFINITY)));
+        if (__ballot(open)) stays = group_stays(tok, L);
         if (p.in_lanes) {
 #pragma unroll
-            for (int i = 0; i < NE; ++i) hi[i] = stays ? hi[i] : 0;
+            for (int i = 0; i < NE; ++i) key[i] = stays ? key[i] : 0;
         } else {
             const uint64_t stay = __ballot(stays);
 #pragma unroll
             for (int i = 0; i < NE; ++i)
-                if (e0 + i < E && !((stay >> (p.per_group.div(e0 + i) * L)) & 1)) hi[i] = 0;
+                if (e0 + i < E && !((stay >> (p.per_group.div(e0 + i) * L)) & 1)) key[i] = 0;
         }
     }
 
     // a threshold that at least k lanes' best keys reach, and few more (fewer than k lanes: 0)
-    uint32_t best = hi[0];
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 1; i < NE; ++i) best = max(best, hi[i]);
+    for (int i = 1; i < NE; ++i) best = max(best, key[i]);
     uint32_t bar = 0;
     for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
         const int n = __popcll(__ballot(best >= (bar | bit)));
@@ -269,91 +390,66 @@ __global__ __launch_bounds__(256) void route_kernel(RouteParams p) {
             if (n <= p.k + 2) break;
         }
     }
+    // The k-th best value is at least the threshold less an error, so what comes out two errors
+    // below is not among them.  (bar can be 0, or a NaN's key: then everything is above.)
+    if (p.bias) {
+        const float v = value_of(bar), w = v - 2 * off(v);
+        bar = w == w ? ordered(w) : 0;
+    }
     bar = max(bar, 1u);
     int before = 0, total = 0;  // picked experts of the lanes before, of all
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-        const uint64_t m = __ballot(hi[i] >= bar);
-        before += __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+        const uint64_t m = __ballot(key[i] >= bar);
+        before = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, before));
         total += __popcll(m);
     }
-    int32_t* ids = p.ids + t * p.k;
-    float* weights = p.weights + t * p.k;
-    if (total <= 64) {
-        // a lane each, in the experts' order
-        uint32_t(*mine)[64] = picked[wave];
+    if (total > 64) return false;
+    // a lane each, in the experts' order
 #pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (hi[i] >= bar) {
-                mine[0][before] = hi[i];
-                mine[1][before] = lo[i];
-                mine[2][before] = (uint32_t)(e0 + i);
-                ++before;
-            }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        const uint64_t key = (uint64_t)mine[0][lane] << 32 | mine[1][lane];
-        const int e = lane < total ? (int)mine[2][lane] : 0;
-        const float x = lane < total ? logit(e) : 0.f;
-        int rank = 0;
+    for (int i = 0; i < NE; ++i)
+        if (key[i] >= bar) mine[before++] = (uint32_t)(e0 + i);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int e = lane < total ? (int)mine[lane] : 0;
+    const float x = tok.logit(e);
+    const double s = tok.score(x) * tok.inv;
+    int rank = 0;
+    if (p.bias) {
+        const uint64_t k = ordered(s + (double)p.bias[e]);
         for (int j = 0; j < total; ++j) {
-            const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(key >> 32), j) << 32 |
-                               (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, j);
-            rank += o > key || (o == key && j < lane) ? 1 : 0;
+            const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(k >> 32), j) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, j);
+            rank += o > k || (o == k && j < lane) ? 1 : 0;
         }
-        const bool chosen = lane < total && rank < p.k;
-        double w = chosen ? score(x) * inv : 0.0;
-        if (p.renorm) {
-            const double sum = wave_sum(w);
-            w = sum == 0 ? 0.0 : w / sum;
+    } else {
+        const uint32_t k = ordered(x);
+        for (int j = 0; j < total; ++j) {
+            const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)k, j);
+            rank += o > k || (o == k && j < lane) ? 1 : 0;
         }
-        if (chosen) {
-            ids[rank] = e;
-            weights[rank] = (float)(w * (double)p.scale);
-        }
-        return;
     }
-    // More than a lane each (many equal keys, or k near the number of lanes): one after the
-    // other, the lowest expert of equals
-    int my_id = 0;
-    for (int r = 0; r < p.k; ++r) {
-        uint64_t mine = 0;
-        int at = 1 << 20;
-#pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const uint64_t k = (uint64_t)hi[i] << 32 | lo[i];
-            const bool is = hi[i] && k > mine;
-            mine = is ? k : mine;
-            at = is ? e0 + i : at;
-        }
-        uint64_t most = mine;
-        for (int x = 32; x > 0; x >>= 1) {
-            const uint64_t o = __shfl_xor((unsigned long long)most, x);
-            most = o > most ? o : most;
-        }
-        const int win = __builtin_amdgcn_readlane(at, __builtin_ctzll(__ballot(mine == most)));  // (lanes hold experts in order)
-#pragma unroll
-        for (int i = 0; i < NE; ++i) hi[i] = e0 + i == win ? 0 : hi[i];
-        if (lane == r) my_id = win;
-    }
-    double w = lane < p.k ? score(logit(my_id)) * inv : 0.0;
-    if (p.renorm) {
-        const double sum = wave_sum(w);
-        w = sum == 0 ? 0.0 : w / sum;
-    }
-    if (lane < p.k) {
-        ids[lane] = my_id;
-        weights[lane] = (float)(w * (double)p.scale);
-    }
+    tok.store(lane < total && rank < p.k, s, e, rank);
+    return true;
+}
+
+template <int NE>
+__global__ __launch_bounds__(256) void route_kernel(RouteParams p) {
+    extern __shared__ float members[];  // [4 waves][E], for groups that do not fill whole lanes
+    __shared__ uint32_t picked[4][64];  // each wave's few
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Token tok{p, (int64_t)blockIdx.x * 4 + wave, 0.f, 1.0};
+    if (tok.t >= p.T) return;  // whole waves; no barrier in what follows
+    if (!route_quickly<NE>(p, tok, members + (int64_t)wave * p.E, picked[wave])) route_slowly(tok);
 }
 
 template <int NE>
 hipError_t go(RouteParams p, hipStream_t st) {
     const int S = p.E / p.groups, lanes = S / NE;
     p.in_lanes = S % NE == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
-    const size_t lds = p.groups > 1 && !p.in_lanes ? (size_t)p.E * 4 * sizeof(double) : 0;
+    const size_t lds = p.groups > 1 && !p.in_lanes ? (size_t)p.E * 4 * sizeof(float) : 0;
     static const hipError_t attr = hipFuncSetAttribute((const void*)route_kernel<NE>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                       64 * NE * 4 * (int)sizeof(double));
+                                                       64 * NE * 4 * (int)sizeof(float));
     if (attr != hipSuccess) return attr;
     hipLaunchKernelGGL((route_kernel<NE>), dim3((unsigned)((p.T + 3) / 4)), dim3(256), lds, st, p);
     return hipGetLastError();
