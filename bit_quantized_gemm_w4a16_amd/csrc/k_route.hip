@@ -59,12 +59,14 @@ __device__ __forceinline__ double from_lane(double v, int lane) {
     const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
     return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
 }
-// Over the wave, in every lane: within 16 lanes by DPP, the four rows' results by readlane.
-__device__ __forceinline__ double wave_sum(double v) {
+// Over the wave, in every lane: within 16 lanes by DPP, the four rows' results by readlane
+// (few: only the first 16 lanes hold anything but 0).
+__device__ __forceinline__ double wave_sum(double v, bool few = false) {
     v += dpp<kXor1>(v);
     v += dpp<kXor2>(v);
     v += dpp<kMirror8>(v);
     v += dpp<kMirror16>(v);
+    if (few) return from_lane(v, 0);
     return (from_lane(v, 0) + from_lane(v, 16)) + (from_lane(v, 32) + from_lane(v, 48));
 }
 __device__ __forceinline__ float wave_max(float v) {
@@ -78,20 +80,25 @@ __device__ __forceinline__ float wave_max(float v) {
 
 // e^x for x <= 0 (NaN: NaN): x = n ln 2 + r, the Taylor series of e^r to r^12 (|r| <= 0.347:
 // the rest is below 2^-52), scaled by 2^n; 20 instructions.
+template <bool LOOP>
 __device__ __forceinline__ double exp_neg(double x) {
+    auto k = [](double v) {  // in a loop: the coefficients made anew, not kept in registers through it
+        if constexpr (LOOP) asm volatile("" : "+s"(v));
+        return v;
+    };
     x = x < -1100.0 ? -1100.0 : x;
     const double n = rint(x * 1.4426950408889634);
-    const double r = fma(-n, 1.9082149292705877e-10, fma(-n, 0.69314718036912382, x));  // ln 2 in two parts
-    double p = 1.0 / 479001600;
-    p = fma(p, r, 1.0 / 39916800);
-    p = fma(p, r, 1.0 / 3628800);
-    p = fma(p, r, 1.0 / 362880);
-    p = fma(p, r, 1.0 / 40320);
-    p = fma(p, r, 1.0 / 5040);
-    p = fma(p, r, 1.0 / 720);
-    p = fma(p, r, 1.0 / 120);
-    p = fma(p, r, 1.0 / 24);
-    p = fma(p, r, 1.0 / 6);
+    const double r = fma(-n, k(1.9082149292705877e-10), fma(-n, k(0.69314718036912382), x));  // ln 2 in two parts
+    double p = k(1.0 / 479001600);
+    p = fma(p, r, k(1.0 / 39916800));
+    p = fma(p, r, k(1.0 / 3628800));
+    p = fma(p, r, k(1.0 / 362880));
+    p = fma(p, r, k(1.0 / 40320));
+    p = fma(p, r, k(1.0 / 5040));
+    p = fma(p, r, k(1.0 / 720));
+    p = fma(p, r, k(1.0 / 120));
+    p = fma(p, r, k(1.0 / 24));
+    p = fma(p, r, k(1.0 / 6));
     p = fma(p, r, 0.5);
     p = fma(p, r, 1.0);
     p = fma(p, r, 1.0);
@@ -99,8 +106,9 @@ __device__ __forceinline__ double exp_neg(double x) {
 }
 // 1 / (1 + e^-x): from t = e^-|x| <= 1, so without overflow; 1 / (1 + t) by two steps of
 // Newton's iteration.
+template <bool LOOP>
 __device__ __forceinline__ double sigmoid(double x) {
-    const double t = exp_neg(-fabs(x)), d = 1.0 + t;
+    const double t = exp_neg<LOOP>(-fabs(x)), d = 1.0 + t;
     double y = __builtin_amdgcn_rcp(d);
     y = fma(fma(-d, y, 1.0), y, y);
     y = fma(fma(-d, y, 1.0), y, y);
@@ -142,15 +150,16 @@ struct Token {
                : p.dtype == HQ_DT_BF16 ? bits16_to_f32<true>(((const uint16_t*)p.logits)[at])
                                        : bits16_to_f32<false>(((const uint16_t*)p.logits)[at]);
     }
+    template <bool LOOP = false>
     __device__ __forceinline__ double score(float x) const {  // not yet times inv
-        if (p.sigmoid) return sigmoid((double)x);
-        return top == -INFINITY && x == top ? 0.0 : exp_neg((double)x - (double)top);
+        if (p.sigmoid) return sigmoid<LOOP>((double)x);
+        return top == -INFINITY && x == top ? 0.0 : exp_neg<LOOP>((double)x - (double)top);
     }
     // The weights of the chosen: lane `chosen` has score w (times inv) of expert e, rank r.
-    __device__ __forceinline__ void store(bool chosen, double w, int e, int r) const {
+    __device__ __forceinline__ void store(bool chosen, double w, int e, int r, bool few = false) const {
         w = chosen ? w : 0.0;
         if (p.renorm) {
-            const double sum = wave_sum(w);
+            const double sum = wave_sum(w, few);
             w = sum == 0 ? 0.0 : sum > 1e-290 ? w * reciprocal(sum) : w / sum;
         }
         if (chosen) {
@@ -163,7 +172,7 @@ struct Token {
 // What ranks expert e.
 __device__ __forceinline__ double rank_value(const Token& tok, int e) {
     const float x = tok.logit(e);
-    return rank_of(tok.p.bias ? tok.score(x) * tok.inv + (double)tok.p.bias[e] : (double)x);
+    return rank_of(tok.p.bias ? tok.score<true>(x) * tok.inv + (double)tok.p.bias[e] : (double)x);
 }
 
 // Whether group lane / L stays, in 64 bits; L lanes to a group look at its members.
@@ -172,12 +181,14 @@ __device__ __forceinline__ bool group_stays(const Token& tok, int L) {
     const int lane = threadIdx.x & 63, S = (int)p.per_group.d, g = lane / L;
     double a = kLowest, b = kLowest;  // the two best, a >= b
     if (g < p.groups)
+#pragma unroll 1
         for (int i = lane % L; i < S; i += L) {
             const int e = g * S + i;
-            const double v = p.bias || p.group_best == 1 ? rank_value(tok, e) : rank_of(tok.score(tok.logit(e)) * tok.inv);
+            const double v = p.bias || p.group_best == 1 ? rank_value(tok, e) : rank_of(tok.score<true>(tok.logit(e)) * tok.inv);
             b = fmax(b, fmin(a, v));
             a = fmax(a, v);
         }
+#pragma unroll 1
     for (int x = 1; x < L; x <<= 1) {
         const double a2 = __shfl_xor(a, x), b2 = __shfl_xor(b, x);
         b = fmax(fmin(a, a2), fmax(b, b2));
@@ -185,6 +196,7 @@ __device__ __forceinline__ bool group_stays(const Token& tok, int L) {
     }
     const double value = p.group_best == 2 ? rank_of(a + b) : a;
     int better = 0;  // fewer than top_groups are better than one that stays (of equals the lower is)
+#pragma unroll 1
     for (int o = 0; o < p.groups; ++o) {
         const double v = from_lane(value, o * L);
         better += v > value || (v == value && o < g) ? 1 : 0;
@@ -205,9 +217,11 @@ __device__ __forceinline__ void route_slowly(const Token& tok) {
     const uint64_t stay = p.groups > 1 ? __ballot(group_stays(tok, L)) : ~0ull;
     uint64_t taken = 0;  // bit i: expert 64 i + lane
     int my_id = 0;
+#pragma unroll 1
     for (int r = 0; r < p.k; ++r) {
         double best = kLowest;
         int at = 1 << 20;
+#pragma unroll 1
         for (int i = 0, e = lane; e < p.E; ++i, e += 64) {
             if (((taken >> i) & 1) || (p.groups > 1 && !((stay >> (p.per_group.div(e) * L)) & 1))) continue;
             const double v = rank_value(tok, e);
@@ -218,6 +232,7 @@ __device__ __forceinline__ void route_slowly(const Token& tok) {
         }
         // the largest, the lowest expert of equals (one is always left: k is at most the
         // experts of the groups that stay)
+#pragma unroll 1
         for (int x = 32; x > 0; x >>= 1) {
             const double v = __shfl_xor(best, x);
             const int o = __shfl_xor(at, x);
@@ -228,7 +243,7 @@ __device__ __forceinline__ void route_slowly(const Token& tok) {
         if (at % 64 == lane) taken |= 1ull << (at / 64);
         if (lane == r) my_id = at;
     }
-    tok.store(lane < p.k, lane < p.k ? tok.score(tok.logit(my_id)) * tok.inv : 0.0, my_id, lane);
+    tok.store(lane < p.k, lane < p.k ? tok.score<true>(tok.logit(my_id)) * tok.inv : 0.0, my_id, lane);
 }
 
 // The quick way; false where it cannot tell.
@@ -264,9 +279,12 @@ __device__ __forceinline__ bool route_quickly(const RouteParams& p, Token& tok, 
                 if (p.bias) bias[i] = p.bias[e0 + i];
             }
     }
-    bool odd = false;  // a NaN among the logits
+    // a NaN among the logits, seen in their sum (so are infinities of both signs: a token that
+    // has them goes the slow way)
+    float all = l[0];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) odd = odd || l[i] != l[i];
+    for (int i = 1; i < NE; ++i) all += l[i];
+    const uint64_t odd = __ballot(all != all);
     // Scores.  Softmax in 64 bits, where the sum over all experts counts (where the weights are
     // renormalised and nothing else asks, it cancels).  Sigmoid: e^-|l| and 1 / (1 + e^-|l|)
     // from the hardware's exp2 and reciprocal (each off by one unit of fp32, the argument
@@ -290,7 +308,12 @@ __device__ __forceinline__ bool route_quickly(const RouteParams& p, Token& tok, 
 #pragma unroll
             for (int i = 0; i < NE; ++i) c[i] = (float)(s[i] * tok.inv);
         }
-        if (__ballot(odd)) tok.inv = __builtin_nan("");  // a NaN is in every weight
+        if (odd) {  // a NaN is in every weight
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) nan = nan || l[i] != l[i];
+            if (__ballot(nan)) tok.inv = __builtin_nan("");
+        }
     } else if (scored) {
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
@@ -305,13 +328,20 @@ __device__ __forceinline__ bool route_quickly(const RouteParams& p, Token& tok, 
     for (int i = 0; i < NE; ++i) {
         if (p.bias) c[i] += bias[i];
         else if (!pairs) c[i] = l[i];
-        key[i] = e0 + i < E ? ordered(p.bias ? c[i] : l[i]) : 0;
+        key[i] = ordered(p.bias ? c[i] : l[i]);
+    }
+    if (E < 64 * NE) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) key[i] = e0 + i < E ? key[i] : 0;
     }
     if (p.bias) {
+        all = c[0];
 #pragma unroll
-        for (int i = 0; i < NE; ++i) odd = odd || c[i] != c[i];
+        for (int i = 1; i < NE; ++i) all += c[i];
+        if (__ballot(all != all)) return false;
+    } else if (odd) {
+        return false;
     }
-    if (__ballot(odd)) return false;
 
     if (p.groups > 1) {
         // the value of a group: the sum of its best one or two; L lanes to a group
@@ -408,35 +438,42 @@ __device__ __forceinline__ bool route_quickly(const RouteParams& p, Token& tok, 
     // a lane each, in the experts' order
 #pragma unroll
     for (int i = 0; i < NE; ++i)
-        if (key[i] >= bar) mine[before++] = (uint32_t)(e0 + i);
+        if (key[i] >= bar) {
+            mine[before] = (uint32_t)(e0 + i);
+            mine[64 + before] = __float_as_uint(l[i]);
+            if (p.bias) mine[128 + before] = __float_as_uint(bias[i]);
+            ++before;
+        }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const int e = lane < total ? (int)mine[lane] : 0;
-    const float x = tok.logit(e);
+    const int e = (int)mine[lane];
+    const float x = __uint_as_float(mine[64 + lane]);
     const double s = tok.score(x) * tok.inv;
+    const uint64_t full = p.bias ? ordered(s + (double)__uint_as_float(mine[128 + lane])) : (uint64_t)ordered(x) << 32;
+    const uint32_t k = lane < total ? (uint32_t)(full >> 32) : 0;  // (0: below every value's)
     int rank = 0;
-    if (p.bias) {
-        const uint64_t k = ordered(s + (double)p.bias[e]);
+    uint64_t equal = 0;  // lanes that have another's upper half
+    for (int j = 0; j < total; ++j) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)k, j);
+        rank += o > k ? 1 : 0;
+        equal |= __ballot(o == k) & ~(1ull << j);
+    }
+    if (equal) {
+        rank = 0;
         for (int j = 0; j < total; ++j) {
-            const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(k >> 32), j) << 32 |
-                               (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, j);
-            rank += o > k || (o == k && j < lane) ? 1 : 0;
-        }
-    } else {
-        const uint32_t k = ordered(x);
-        for (int j = 0; j < total; ++j) {
-            const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)k, j);
-            rank += o > k || (o == k && j < lane) ? 1 : 0;
+            const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(full >> 32), j) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)full, j);
+            rank += o > full || (o == full && j < lane) ? 1 : 0;
         }
     }
-    tok.store(lane < total && rank < p.k, s, e, rank);
+    tok.store(lane < total && rank < p.k, s, e, rank, total <= 16);
     return true;
 }
 
 template <int NE>
 __global__ __launch_bounds__(256) void route_kernel(RouteParams p) {
     extern __shared__ float members[];  // [4 waves][E], for groups that do not fill whole lanes
-    __shared__ uint32_t picked[4][64];  // each wave's few
+    __shared__ uint32_t picked[4][3 * 64];  // each wave's few: expert, logit, bias
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Token tok{p, (int64_t)blockIdx.x * 4 + wave, 0.f, 1.0};
     if (tok.t >= p.T) return;  // whole waves; no barrier in what follows
