@@ -494,6 +494,8 @@ hipError_t go(RouteParams p, hipStream_t st) {
 
 // ---- the weighted sum ----
 
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 // place[p] = the row that holds pair p (rows sorted by expert).
 __global__ __launch_bounds__(256) void place_kernel(const int32_t* __restrict__ sorted, int64_t P, int32_t* __restrict__ place) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -502,60 +504,125 @@ __global__ __launch_bounds__(256) void place_kernel(const int32_t* __restrict__ 
     if (p >= 0 && p < P) place[p] = (int32_t)i;
 }
 
+// Up to so many pairs, each token's workgroup looks through `sorted` for its rows itself: a
+// launch less (8 experts, 7168 columns, 5 tokens: 4.9 us, with a launch for the places
+// 7.9; 100 tokens: 6.7, 7.9).
+constexpr int kCombineFew = 1024;
+
 struct CombineParams {
     const uint16_t *y, *add;
     const float* weights;
-    const int32_t *sorted, *place;
+    const int32_t *sorted, *place;  // place NULL: of few pairs
     uint16_t* out;
     int64_t N, P;
     int k;
 };
 
-// out[t] = rnd16(add[t] + sum_j w[t][j] y[row(t, j)]), j in order, fp32.  Bound by HBM:
-// a thread sums 8 columns (VEC: 16-byte loads) over the token's rows.  A row of
-// weight 0 is not read.
-template <bool BF16, bool VEC>
-__global__ __launch_bounds__(256) void combine_kernel(CombineParams p) {
-    const int64_t t = blockIdx.x;
-    const int64_t n = ((int64_t)blockIdx.y * 256 + threadIdx.x) * (VEC ? 8 : 1);
+// out[t] = rnd16(add[t] + sum_j w[t][j] y[row(t, j)]), j in order, fp32.  Bound by HBM, so
+// what matters is how many loads are on their way: a workgroup takes a token, its lanes
+// look up the token's rows side by side, and a thread then has the loads of eight rows
+// under way at a time (8 columns each, VEC: 16 bytes).  A row of weight 0 is not read.
+template <bool BF16, bool VEC, bool NT, int R>
+__device__ __forceinline__ void add_rows(const CombineParams& p, uint64_t& left, int64_t row, float w, int64_t n, float (&acc)[VEC ? 8 : 1]) {
+    v4u v[R];
+    uint32_t one[R];
+    float wj[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {  // the next R rows that count
+        const int j = __builtin_ctzll(left);
+        left &= left - 1;
+        const int64_t at = (int64_t)__builtin_amdgcn_readlane((int)row, j);
+        wj[r] = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(w), j));
+        if constexpr (VEC && NT) v[r] = ld_nt((const v4u*)(p.y + at * p.N + n));
+        else if constexpr (VEC) v[r] = ld16(p.y + at * p.N + n);
+        else one[r] = p.y[at * p.N + n];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t u = v[r][i];
+                acc[2 * i] += wj[r] * bits16_to_f32<BF16>((uint16_t)u);
+                acc[2 * i + 1] += wj[r] * bits16_to_f32<BF16>((uint16_t)(u >> 16));
+            }
+        } else {
+            acc[0] += wj[r] * bits16_to_f32<BF16>((uint16_t)one[r]);
+        }
+    }
+}
+
+template <bool BF16, bool VEC, bool NT>
+__global__ __launch_bounds__(512) void combine_kernel(CombineParams p) {
     constexpr int C = VEC ? 8 : 1;
-    float acc[C] = {};
-    if (n >= p.N) return;
-    for (int j = 0; j < p.k; ++j) {
-        const int64_t pair = t * p.k + j;
-        const float w = p.weights[pair];
-        int64_t row = pair;
-        bool have = w != 0.f;
-        if (p.sorted) {
+    __shared__ int row_of[kCombineFew];
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 63;
+    if (p.sorted && !p.place) {  // (then k is at most kCombineFew)
+        for (int j = threadIdx.x; j < p.k; j += blockDim.x) row_of[j] = -1;
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.P; i += blockDim.x) {
+            const int64_t j = p.sorted[i] - t * p.k;
+            if (j >= 0 && j < p.k) row_of[j] = i;
+        }
+        __syncthreads();
+    }
+    // the token's first 64 pairs: lane j's row (each wave for itself)
+    float w0 = 0.f;
+    int64_t row0 = 0;
+    auto look = [&](int j0, float& w, int64_t& row) -> uint64_t {
+        const int j = j0 + lane;
+        bool have = j < p.k;
+        const int64_t pair = t * p.k + (have ? j : 0);
+        w = have ? p.weights[pair] : 0.f;
+        row = pair;
+        have = have && w != 0.f;
+        if (p.sorted && !p.place) {
+            row = have ? row_of[j] : -1;
+            have = row >= 0;
+        } else if (p.sorted) {
             // a pair that no row names has whatever the workspace held: it counts only if
             // its row names it
             row = p.place[pair];
-            have = have && row >= 0 && row < p.P && p.sorted[row] == (int32_t)pair;
+            const bool in = row >= 0 && row < p.P;
+            have = have && in && p.sorted[in ? row : 0] == (int32_t)pair;
         }
-        if (!have) continue;
+        return __ballot(have);
+    };
+    const uint64_t have0 = look(0, w0, row0);
+    for (int64_t n0 = (int64_t)blockIdx.y * blockDim.x; n0 * C < p.N; n0 += (int64_t)gridDim.y * blockDim.x) {
+        const int64_t n = (n0 + threadIdx.x) * C;
+        const bool live = n < p.N;
+        const int64_t nl = live ? n : 0;  // (past the row: its start, not stored)
+        v4u a = v4u{0, 0, 0, 0};
+        uint32_t a1 = 0;
+        if (p.add) {
+            if constexpr (VEC) a = ld16(p.add + t * p.N + nl);
+            else a1 = p.add[t * p.N + nl];
+        }
+        float acc[C] = {};
+        for (int j0 = 0; j0 < p.k; j0 += 64) {
+            float w = w0;
+            int64_t row = row0;
+            uint64_t left = j0 ? look(j0, w, row) : have0;
+            while (__popcll(left) >= 8) add_rows<BF16, VEC, NT, 8>(p, left, row, w, nl, acc);
+            if (__popcll(left) >= 4) add_rows<BF16, VEC, NT, 4>(p, left, row, w, nl, acc);
+            if (__popcll(left) >= 2) add_rows<BF16, VEC, NT, 2>(p, left, row, w, nl, acc);
+            if (left) add_rows<BF16, VEC, NT, 1>(p, left, row, w, nl, acc);
+        }
+        if (!live) continue;
         if constexpr (VEC) {
-            const v4u v = ld16(p.y + row * p.N + n);
+            v4u o;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t u = v[i];
-                acc[2 * i] += w * bits16_to_f32<BF16>((uint16_t)u);
-                acc[2 * i + 1] += w * bits16_to_f32<BF16>((uint16_t)(u >> 16));
+                const uint32_t u = a[i];
+                const float x = acc[2 * i] + bits16_to_f32<BF16>((uint16_t)u), y = acc[2 * i + 1] + bits16_to_f32<BF16>((uint16_t)(u >> 16));
+                o[i] = (uint32_t)f32_to_16<BF16>(x) | ((uint32_t)f32_to_16<BF16>(y) << 16);
             }
+            *(v4u*)(p.out + t * p.N + n) = o;
         } else {
-            acc[0] += w * bits16_to_f32<BF16>(p.y[row * p.N + n]);
+            p.out[t * p.N + n] = f32_to_16<BF16>(acc[0] + bits16_to_f32<BF16>((uint16_t)a1));
         }
-    }
-    if constexpr (VEC) {
-        v4u o = p.add ? ld16(p.add + t * p.N + n) : v4u{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t u = o[i];
-            const float a = acc[2 * i] + bits16_to_f32<BF16>((uint16_t)u), b = acc[2 * i + 1] + bits16_to_f32<BF16>((uint16_t)(u >> 16));
-            o[i] = (uint32_t)f32_to_16<BF16>(a) | ((uint32_t)f32_to_16<BF16>(b) << 16);
-        }
-        *(v4u*)(p.out + t * p.N + n) = o;
-    } else {
-        p.out[t * p.N + n] = f32_to_16<BF16>(acc[0] + (p.add ? bits16_to_f32<BF16>(p.add[t * p.N + n]) : 0.f));
     }
 }
 
@@ -600,18 +667,29 @@ hipError_t route_launch(const RouteArgs& a) {
 
 hipError_t combine_launch(const CombineArgs& a) {
     const int64_t P = a.T * a.top_k;
-    if (a.sorted) {
+    const bool few = P <= kCombineFew;
+    if (a.sorted && !few) {
         hipLaunchKernelGGL(place_kernel, dim3((unsigned)((P + 255) / 256)), dim3(256), 0, a.stream, a.sorted, P, a.place);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    CombineParams p{(const uint16_t*)a.y, (const uint16_t*)a.add, a.weights, a.sorted, a.place, (uint16_t*)a.out, a.N, P, a.top_k};
+    CombineParams p{(const uint16_t*)a.y, (const uint16_t*)a.add, a.weights, a.sorted, few ? nullptr : a.place, (uint16_t*)a.out, a.N, P, a.top_k};
     const bool vec = a.N % 8 == 0;
-    const dim3 grid((unsigned)a.T, (unsigned)((a.N + (vec ? 2047 : 255)) / (vec ? 2048 : 256)));
-    if (vec && a.bf16) hipLaunchKernelGGL((combine_kernel<true, true>), grid, dim3(256), 0, a.stream, p);
-    else if (vec) hipLaunchKernelGGL((combine_kernel<false, true>), grid, dim3(256), 0, a.stream, p);
-    else if (a.bf16) hipLaunchKernelGGL((combine_kernel<true, false>), grid, dim3(256), 0, a.stream, p);
-    else hipLaunchKernelGGL((combine_kernel<false, false>), grid, dim3(256), 0, a.stream, p);
+    // a workgroup for a token, of as many threads as share its columns evenly; for few
+    // tokens, which do not fill the chip, one for each 128 threads' columns (7168 columns, 5
+    // tokens: 3.2 us, one workgroup each 4.6; 60: 3.7, 4.9)
+    const int64_t units = vec ? a.N / 8 : a.N, turns = ceil_div(units, 512);
+    const int threads = a.T < 64 ? 128 : (int)ceil_div(ceil_div(units, turns), 64) * 64;
+    const dim3 grid((unsigned)a.T, (unsigned)(a.T < 64 ? ceil_div(units, threads) : 1)), block(threads);
+    // Rows that the 256 MB behind the L2s cannot hold go past them (y of 470 MB: 99 us, loaded
+    // as others are 122; of 115 MB, just written: 29, 26)
+    const bool nt = P * a.N * 2 > (int64_t)256 << 20;
+    if (vec && a.bf16 && nt) hipLaunchKernelGGL((combine_kernel<true, true, true>), grid, block, 0, a.stream, p);
+    else if (vec && a.bf16) hipLaunchKernelGGL((combine_kernel<true, true, false>), grid, block, 0, a.stream, p);
+    else if (vec && nt) hipLaunchKernelGGL((combine_kernel<false, true, true>), grid, block, 0, a.stream, p);
+    else if (vec) hipLaunchKernelGGL((combine_kernel<false, true, false>), grid, block, 0, a.stream, p);
+    else if (a.bf16) hipLaunchKernelGGL((combine_kernel<true, false, false>), grid, block, 0, a.stream, p);
+    else hipLaunchKernelGGL((combine_kernel<false, false, false>), grid, block, 0, a.stream, p);
     return hipGetLastError();
 }
 
