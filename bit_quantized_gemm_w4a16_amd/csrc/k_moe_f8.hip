@@ -2,9 +2,9 @@
 //
 //   D[p][n] = sum_b sa[a][b] sw[e][b][n / 128] sum_{k in block b} A[a][k] W[e][k][n]
 //
-// with blocks of 128 along K, E4M3 codes on the scaled MFMA (unit scales: the
-// instruction's own scales are powers of two), one 16 x 16 x 128 product per block,
-// each product scaled in fp32 and added to the fp32 sum, one rounding to bf16.  Inside
+// with blocks of 128 along K, E4M3 codes on the MFMA of 8-bit types in its unscaled form
+// (its own scales are powers of two), one 16 x 16 x 128 product per block, each product
+// scaled in fp32 and added to the fp32 sum, one rounding to bf16.  Inside
 // a block the instruction cuts the products of 8 neighbouring K to 13 bits below the
 // largest one's power of two before it adds them (measured on gfx950, the unscaled
 // 16 x 16 x 32 form too): 2^-18.6 of the block's sum of absolute values rms, 1/50 of
@@ -15,7 +15,7 @@
 // the offsets by itself; above, a counting sort by expert and the tile list come
 // first: one workgroup up to kF8Chunk pairs, else histograms of chunks in one launch,
 // and a second in which each chunk's workgroup sums the histograms for itself and
-// places its pairs (32760 pairs: 11 us; with launches of their own for the scan and the
+// places its pairs (32760 pairs: 14 us; with launches of their own for the scan and the
 // ranks 17).  Rows of an expert come in any order: a row's sums do not depend on its
 // place.
 #include "hq_device.hpp"
@@ -473,6 +473,11 @@ struct F8Stage {
     float* sa;
 };
 
+template <class F, int... I>
+__device__ __forceinline__ void each_of(F& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+
 template <int MT>
 __device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int tn, int* rowD, const F8Stage& st) {
     constexpr int NT = 4, H = MT >= 6 ? 4 : 2;                       // strips of a wave; subtiles of A1
@@ -485,11 +490,12 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int
     const rsrc_t rA = make_rsrc(p.A, (uint32_t)(p.a_rows * p.K));
     const rsrc_t rS = make_rsrc(p.S + (int64_t)tile.expert * p.s_estride, (uint32_t)(p.s_estride * 4));
     const rsrc_t rSA = make_rsrc(p.sa, (uint32_t)(p.a_rows * nb * 4));
-    // wave w loads the strips 2 w and 2 w + 1 (past the last: zeros, they lie behind the resource)
-    const uint32_t strip_bytes = (uint32_t)nb * 2048u, strip0 = (uint32_t)(tn * 16 + wave * 2) * strip_bytes, boff = (uint32_t)lane * 16u;
+    // wave w loads the strips 2 w and 2 w + 1 (past the last: that one, for columns that are not stored)
+    const uint32_t strip_bytes = (uint32_t)nb * 2048u, boff = (uint32_t)lane * 16u;
+    const uint32_t strip[2] = {min((uint32_t)(tn * 16 + wave * 2), p.strips - 1u) * strip_bytes, min((uint32_t)(tn * 16 + wave * 2 + 1), p.strips - 1u) * strip_bytes};
 #pragma unroll
     for (int n = 0; n < LB; ++n)  // (block 0's weights: they need no row)
-        dma16(rW, (lds_char*)st.b[0] + wave * 4096 + n * 1024, boff, strip0 + (n >> 1) * strip_bytes + (n & 1) * 1024u);
+        dma16(rW, (lds_char*)st.b[0] + wave * 4096 + n * 1024, boff, strip[n >> 1] + (n & 1) * 1024u);
     // 16-byte slot i * 512 + tid of A1 and A2 together: row slot / 8, and of it the unit
     // slot % 8 ^ (row >> 1 & 7), which spreads the reads of 16 rows over the banks
     uint32_t aoff[L1 + L2];
@@ -505,7 +511,7 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int
     auto load_m = [&](int blk, int s, int n) {
         const int at = min(blk, nb - 1);
         if (n < LB)
-            dma16(rW, (lds_char*)st.b[s] + wave * 4096 + n * 1024, boff, strip0 + (uint32_t)at * 2048u + (n >> 1) * strip_bytes + (n & 1) * 1024u);
+            dma16(rW, (lds_char*)st.b[s] + wave * 4096 + n * 1024, boff, strip[n >> 1] + (uint32_t)at * 2048u + (n & 1) * 1024u);
         else
             dma16(rA, (lds_char*)st.a1[s] + wave * 1024 + (n - LB) * 8192, aoff[n - LB], (uint32_t)at * 128u);
     };
@@ -584,8 +590,7 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, const Tile& tile, int
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
-        auto all = [&]<int... I>(std::integer_sequence<int, I...>) { (subtile(std::integral_constant<int, I>{}), ...); };
-        all(std::make_integer_sequence<int, MT>{});
+        each_of(subtile, std::make_integer_sequence<int, MT>{});
     };
     using S0 = std::integral_constant<int, 0>;
     using S1 = std::integral_constant<int, 1>;
