@@ -582,7 +582,8 @@ hq_status hq_silu_mul_quant(int32_t dtype, int32_t out_dtype, int32_t a_scale, i
  *   ranking  by c_e = s_e + bias_e; without a bias by the logits
  *   groups   (groups > 1) of num_experts / groups neighbouring experts: only those of
  *            the top_groups groups of the largest value can be chosen; a group's value
- *            is the sum of its group_best (1 or 2) largest c_e (s_e without a bias)
+ *            is that of its best expert in the ranking (group_best 1) or the sum of its
+ *            two largest c_e (2; s_e without a bias)
  *   chosen   the top_k largest of the ranking, in descending order
  *   weights  scale * s_e, divided first by the sum of the chosen s_e if renormalize
  * Scores are formed and compared in 64 bits, and equal values (of experts and of

@@ -54,7 +54,8 @@ def route(logits, bias, top_k, sigmoid, renormalize, groups=1, top_groups=1, gro
     c = np.where(np.isnan(c), -np.inf, c)
     allowed = np.ones((T, E), bool)
     if groups > 1:
-        v = (s if bias is None else c).reshape(T, groups, E // groups)
+        # (the best one by the ranking: without a bias by the logits, which differ where scores round alike)
+        v = (s if bias is None and group_best == 2 else c).reshape(T, groups, E // groups)
         value = np.sort(v, axis=2)[:, :, ::-1][:, :, :group_best].sum(2)
         best = np.argsort(-value, axis=1, kind="stable")[:, :top_groups]
         stay = np.zeros((T, groups), bool)
