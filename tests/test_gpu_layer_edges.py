@@ -1,0 +1,252 @@
+"""A routed layer's operators where their ways change: sizes past a tile, a cache or 31 bits, values that fp32
+cannot tell apart, scales at the ends of the range, calls at the same time."""
+import numpy as np
+import pytest
+import torch
+
+import synthetic as syn
+from bit_quantized_gemm_w4a16_amd import hq
+from gpu_util import note
+from layer_util import DT, FORMS, SILU_DELTA, check_rows, f64, outputs, run_norm
+from oracle import layer as ol
+from test_gpu_moe_f8 import Experts, both_ways
+from test_gpu_route import check, logits_of, summed
+
+pytestmark = pytest.mark.gpu
+
+
+def swiglu(form, dtype, gate_up, rows, I):
+    odt, kind, _, _ = FORMS[form]
+    out = outputs(form, dtype, rows, I)
+    hq.hq_silu_mul_quant(DT[dtype][0], odt, kind, rows, I, gate_up, out[0], out[1])
+    torch.cuda.synchronize()
+    return out
+
+
+# ---------------------------------------------------------------------------
+# SwiGLU
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_swiglu_gates_of_every_size(dtype):
+    """One gate value for each block of 128, -84 to 84: its scale has 24 bits of it."""
+    note(f"swiglu gates {dtype}")
+    M, I = 40, 1280
+    g = torch.linspace(-84, 84, M * I // 128).view(M, -1).repeat_interleave(128, 1)
+    if dtype == "bf16":
+        u = torch.randn(M, I, generator=torch.Generator().manual_seed(0))
+    else:
+        u = torch.randn(M, I, generator=torch.Generator().manual_seed(0)) * 100
+    gu = torch.cat([g, u], 1).to(DT[dtype][1]).cuda()
+    check_rows("f8_block", dtype, ol.silu_mul(f64(gu)), SILU_DELTA, *swiglu("f8_block", dtype, gu, M, I))
+
+
+@pytest.mark.parametrize("form", ["f8_token", "i8_token", "f8_block"])
+def test_swiglu_scales_that_are_denormals(form):
+    """A largest value of 590 units of 2^-149: its scale is one unit (E4M3), and the codes stop at the largest."""
+    note(f"swiglu denormal scales {form}")
+    gu = torch.zeros(2, 2 * 256)
+    gu[:, :256] = -20.0  # silu: -4.1e-8
+    gu[0, 256:] = torch.linspace(0.0, 2e-35, 256)
+    gu[1, 256:] = -2e-35
+    y = ol.silu_mul(f64(gu.to(torch.bfloat16)))
+    assert (np.abs(y[0]).max() / 2.0 ** -149 > 500) and (np.abs(y).max() / 2.0 ** -149 < 660)
+    out, scale, n, ns = swiglu(form, "bf16", gu.to(torch.bfloat16).cuda(), 2, 256)
+    s = f64(scale[:ns].view(torch.float32))
+    assert (s > 0).all() and (s <= 8 * 2.0 ** -149).all()
+    top = FORMS[form][3]
+    codes = f64(out[:n].view(torch.int8 if form == "i8_token" else torch.float8_e4m3fn)).reshape(2, 256)
+    assert np.isfinite(codes).all() and (np.abs(codes).max() == top or form == "i8_token") and (codes[0] <= 0).all() and (codes[1] >= 0).all()
+
+
+def test_swiglu_of_infinities():
+    """silu(inf) = inf, silu(-inf) = NaN by its formula; with an infinite maximum finite values have the code 0."""
+    note("swiglu infinities")
+    gu = torch.ones(4, 2 * 256)
+    gu[0, 3], gu[1, 3], gu[2, 3], gu[3, 3 + 256] = torch.inf, -torch.inf, torch.nan, -torch.inf
+    out, scale, n, ns = swiglu("f8_token", "bf16", gu.to(torch.bfloat16).cuda(), 4, 256)
+    s, codes = scale[:ns].view(torch.float32).cpu(), out[:n].view(4, 256).cpu()
+    assert (codes[:, 3] == 0x7F).all()
+    rest = codes[:, [i for i in range(256) if i != 3]]
+    assert (rest[[0, 3]] == 0).all() and (rest[[1, 2]] == 0x7E).all()
+    assert s[0] == torch.inf and s[3] == torch.inf and torch.isfinite(s[1:3]).all()
+
+
+# ---------------------------------------------------------------------------
+# rows past 31 bits
+# ---------------------------------------------------------------------------
+
+def test_norm_past_31_bits():
+    note("norm 32776 x 65536")
+    M, K = 32776, 65536
+    x = torch.randn(64, K, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).cuda().repeat(513, 1)[:M]
+    w = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    out, scale, n, ns = run_norm("f8_block", "bf16", x, None, w, M, K)
+    few, fs, fn, fns = run_norm("f8_block", "bf16", x[:64], None, w, 64, K)
+    torch.cuda.synchronize()
+    got, want = out[:n].view(M, K), few[:fn].view(64, K)
+    for first in (0, 16384, 32768 - 64):
+        assert torch.equal(got[first:first + 64], want)
+    assert torch.equal(got[32768:], want[:8]) and torch.equal(scale[:ns].view(M, -1)[32768:], fs[:fns].view(64, -1)[:8])
+
+
+def test_route_past_31_bits():
+    note("route 524300 x 4096")
+    T, E = 524300, 4096
+    few = logits_of(1, 50, E, "bf16")
+    x = few.repeat(T // 50, 1)
+    desc = hq.route_desc(hq.HQ_DT_BF16, E, 8)
+    ids, w = torch.empty(T, 8, dtype=torch.int32, device="cuda"), torch.empty(T, 8, device="cuda")
+    hq.hq_moe_route(desc, T, x, E, None, ids, w)
+    want, ww = torch.empty(50, 8, dtype=torch.int32, device="cuda"), torch.empty(50, 8, device="cuda")
+    hq.hq_moe_route(desc, 50, few, E, None, want, ww)
+    assert torch.equal(ids.view(-1, 50, 8), want.expand(T // 50, 50, 8)) and torch.equal(w.view(-1, 50, 8), ww.expand(T // 50, 50, 8))
+
+
+@pytest.mark.parametrize("T,k,N", [(4200, 5, 7168), (15100, 20, 7168)])
+@pytest.mark.parametrize("ordered", [False, True])
+def test_combine_past_the_cache_and_31_bits(T, k, N, ordered):
+    note(f"combine T={T} k={k} N={N} sorted={ordered}")
+    P = T * k
+    g = torch.Generator(device="cuda").manual_seed(T)
+    y = torch.randn(P, N, generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.rand(T, k, generator=g, device="cuda")
+    order = torch.randperm(P, generator=g, device="cuda").to(torch.int32) if ordered else None
+    at = torch.arange(P, device="cuda")
+    if ordered:
+        at[order.long()] = torch.arange(P, device="cuda")
+    out = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    hq.hq_moe_combine(hq.HQ_DT_BF16, T, k, N, y, w, out, sorted_pairs=order, workspace=torch.empty(P, dtype=torch.int32, device="cuda") if ordered else None, ws_bytes=4 * P)
+    for t in [*range(0, T, T // 40), T - 1]:
+        rows = y[at.view(T, k)[t]].double() * w[t].double()[:, None]
+        want, S = rows.sum(0), rows.abs().sum(0)
+        assert ((out[t].double() - want).abs() <= want.abs() * 2.0 ** -8 + S * (2 * k + 2) * 2.0 ** -24).all(), t
+
+
+def test_experts_past_32_bits():
+    """Weights of 4.4 GB, activations of 3.8, results of 4.3: the last expert's rows are what it gives alone."""
+    note("experts f8 150 x 4096 x 7168")
+    E, N, K, T = 150, 4096, 7168, 90
+    one, many = hq.desc_moe_fp8_blockwise(1, N, K), hq.desc_moe_fp8_blockwise(E, N, K)
+    wp, sp, _ = hq.hq_repack(one, np.zeros((1, K, N), np.uint8), np.ones((1, K // 128, N // 128), np.float32))
+    g = torch.Generator(device="cuda").manual_seed(0)
+    wp = torch.randint(0, 256, (E, wp.nbytes), generator=g, device="cuda", dtype=torch.uint8) & 0xBF  # (no NaN)
+    sp = torch.rand(E, sp.nbytes // 4, generator=g, device="cuda") * 1e-2
+    a = torch.randint(0, 256, (T, K), generator=g, device="cuda", dtype=torch.uint8) & 0xBF
+    sa = torch.rand(T, K // 128, generator=g, device="cuda")
+
+    def run(desc, a, sa, ids, w, s):
+        T = len(a)
+        n = hq.hq_workspace_bytes(desc, T, 1)
+        out = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+        hq.hq_moe_gemm(desc, hq.HQ_MOE_INDEXED, T, 1, a, sa, ids, None, w, s, None, out, torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+        torch.cuda.synchronize()
+        return out
+
+    zero = torch.zeros(T, dtype=torch.int32, device="cuda")
+    alone = run(one, a, sa, zero, wp[E - 1], sp[E - 1])
+    assert torch.isfinite(alone.float()).all() and alone.float().abs().max() > 0
+    assert torch.equal(run(many, a, sa, zero + E - 1, wp, sp), alone)
+    assert torch.equal(run(many, a[:3], sa[:3], zero[:3] + E - 1, wp, sp), alone[:3])
+    note("experts f8 524250 rows")  # as many as fit below 2^31 elements of D, in copies of the same 90
+    copies = 5825
+    big = run(one, a.repeat(copies, 1), sa.repeat(copies, 1), zero.repeat(copies), wp[E - 1], sp[E - 1])
+    for at in (0, 2912, copies - 1):
+        assert torch.equal(big[90 * at:90 * at + 90], alone)
+
+
+# ---------------------------------------------------------------------------
+# routing's close calls
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("best", [1, 2])
+def test_route_groups_that_are_nearly_equal(sigmoid, best):
+    """Groups that hold the same logits in another order, and ones a few units in the last place apart."""
+    note(f"route near groups sigmoid={sigmoid} best={best}")
+    rng = np.random.default_rng(1)
+    T, G, n = 64, 8, 32
+    base = rng.standard_normal((T, 1, n)).astype(np.float32)
+    x = np.stack([np.stack([rng.permutation(base[t, 0]) for _ in range(G)]) for t in range(T)])
+    x[T // 2:] *= (1 + rng.integers(-2, 3, (T // 2, G, 1)) * np.float32(2.0 ** -23)).astype(np.float32)
+    x = torch.from_numpy(np.ascontiguousarray(x.reshape(T, G * n))).cuda()
+    bias = torch.from_numpy(np.tile(0.1 * rng.standard_normal(1).astype(np.float32), G * n)).cuda()
+    for b in (None, bias):
+        check(x, b, 8, sigmoid=sigmoid, groups=G, top_groups=3, group_best=best)
+
+
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e8, 1e30])
+def test_route_large_biases(size):
+    note(f"route bias {size}")
+    b = torch.full((256,), size)
+    b[::3] = float(np.nextafter(np.float32(size), np.float32(np.inf)))
+    x = logits_of(2, 30, 256)
+    for sigmoid in (False, True):
+        check(x, b.cuda(), 8, sigmoid=sigmoid)
+        check(x, b.cuda(), 8, sigmoid=sigmoid, groups=8, top_groups=3, group_best=2)
+        check(x, -b.cuda(), 60, sigmoid=sigmoid)
+
+
+def test_route_wide_logits_and_many_equal():
+    note("route wide logits")
+    x = logits_of(3, 20, 4096)
+    x[:5] *= 1e30
+    x[5:10] = torch.randint(0, 3, (5, 4096), generator=torch.Generator().manual_seed(1)).float().cuda()
+    x[10:15] = torch.finfo(torch.float32).max * torch.randint(-1, 2, (5, 4096), generator=torch.Generator().manual_seed(2)).float().cuda()
+    for kw in (dict(), dict(sigmoid=True), dict(groups=64, top_groups=3, group_best=2), dict(sigmoid=True, groups=64, top_groups=9)):
+        check(x, None, 64, **kw)
+
+
+# ---------------------------------------------------------------------------
+# the weighted sum's ways
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,k,N", [(2, 700, 40), (3, 100, 512), (129, 8, 64), (200, 8, 777), (1030, 1, 128), (70, 64, 2048), (513, 2, 8)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_combine_many_pairs(dtype, T, k, N):
+    """More pairs than a workgroup looks through by itself, more rows of a token than a wave holds; garbage in the workspace."""
+    g = torch.Generator().manual_seed(T)
+    y = torch.randn(T * k, N, generator=g).to(DT[dtype][1]).cuda()
+    w = (torch.rand(T, k, generator=g) - 0.2).cuda()
+    order = torch.randperm(T * k, generator=g).to(torch.int32)
+    order[5], order[17] = -3, 1 << 29  # two rows that belong to no pair
+    at = np.full(T * k, -1, np.int64)
+    o = order.numpy()
+    ok = (o >= 0) & (o < T * k)
+    at[o[ok]] = np.nonzero(ok)[0]
+    for rows, dev in ((np.arange(T * k), None), (at, order.cuda())):
+        note(f"combine {dtype} T={T} k={k} N={N} sorted={dev is not None}")
+        got = summed(dtype, y, w, None, dev, T, k, N)
+        want, S = ol.combine(f64(y), f64(w), None, rows.reshape(T, k))
+        assert (np.abs(got - want) <= np.abs(want) * DT[dtype][2] + S * (2 * k + 2) * 2.0 ** -24 + 2.0 ** -25).all()
+
+
+# ---------------------------------------------------------------------------
+# experts
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,E,N", [(1537, 1, 300), (2100, 3, 520), (2600, 1, 257)])
+def test_experts_with_more_rows_than_a_group_of_tiles(rows, E, N):
+    note(f"experts f8 rows={rows} E={E} N={N}")
+    x = Experts(E, N, 256, seed=rows)
+    both_ways(x, rows, 1, np.full((rows, 1), E - 1, np.int32), 3)
+
+
+def test_experts_on_two_streams():
+    """Calls at the same time, each with its own workspace."""
+    note("experts f8 two streams")
+    x = Experts(6, 512, 1024)
+    jobs = []
+    for T, k, seed in ((300, 2, 1), (5, 2, 2)):
+        a, sa = x.rows(T, seed)
+        ids = torch.from_numpy(syn.zipf_topk(seed, 5, T, 6, k).astype(np.int32)).cuda()
+        want = x.call(hq.HQ_MOE_INDEXED, T, k, a, sa, ids, None).clone()
+        ws = torch.zeros(hq.hq_workspace_bytes(x.desc, T, k), dtype=torch.uint8, device="cuda")
+        jobs.append((T, k, a, sa, ids, want, torch.empty_like(want), ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for T, k, a, sa, ids, want, out, ws, st in jobs:
+            x.call(hq.HQ_MOE_INDEXED, T, k, a, sa, ids, None, out=out, ws=ws, stream=st.cuda_stream)
+    torch.cuda.synchronize()
+    for *_, want, out, ws, st in jobs:
+        assert torch.equal(out, want)
