@@ -59,14 +59,15 @@ __device__ __forceinline__ double from_lane(double v, int lane) {
     const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
     return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
 }
-// Over the wave, in every lane: within 16 lanes by DPP, the four rows' results by readlane
-// (few: only the first 16 lanes hold anything but 0).
-__device__ __forceinline__ double wave_sum(double v, bool few = false) {
+// Over 16 lanes, and over the wave: within 16 lanes by DPP, the four rows' results by readlane.
+__device__ __forceinline__ double row_sum(double v) {
     v += dpp<kXor1>(v);
     v += dpp<kXor2>(v);
     v += dpp<kMirror8>(v);
-    v += dpp<kMirror16>(v);
-    if (few) return from_lane(v, 0);
+    return v + dpp<kMirror16>(v);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    v = row_sum(v);
     return (from_lane(v, 0) + from_lane(v, 16)) + (from_lane(v, 32) + from_lane(v, 48));
 }
 __device__ __forceinline__ float wave_max(float v) {
@@ -155,11 +156,13 @@ struct Token {
         if (p.sigmoid) return sigmoid<LOOP>((double)x);
         return top == -INFINITY && x == top ? 0.0 : exp_neg<LOOP>((double)x - (double)top);
     }
-    // The weights of the chosen: lane `chosen` has score w (times inv) of expert e, rank r.
-    __device__ __forceinline__ void store(bool chosen, double w, int e, int r, bool few = false) const {
+    // The weights of the chosen: lane `chosen` has score w (times inv) of expert e, rank r; the
+    // token's lanes are a wave, or 16 (ROW).
+    template <bool ROW = false>
+    __device__ __forceinline__ void store(bool chosen, double w, int e, int r) const {
         w = chosen ? w : 0.0;
         if (p.renorm) {
-            const double sum = wave_sum(w, few);
+            const double sum = ROW ? row_sum(w) : wave_sum(w);
             w = sum == 0 ? 0.0 : sum > 1e-290 ? w * reciprocal(sum) : w / sum;
         }
         if (chosen) {
@@ -167,6 +170,16 @@ struct Token {
             p.weights[t * p.k + r] = (float)(w * (double)p.scale);
         }
     }
+};
+
+// A token's few experts that are left, in their order, for a lane each; how many they are, and
+// what the scores need.
+struct Few {
+    uint32_t expert[64];
+    float logit[64], bias[64];
+    int count;
+    float top;
+    double inv;
 };
 
 // What ranks expert e.
@@ -246,9 +259,9 @@ __device__ __forceinline__ void route_slowly(const Token& tok) {
     tok.store(lane < p.k, lane < p.k ? tok.score<true>(tok.logit(my_id)) * tok.inv : 0.0, my_id, lane);
 }
 
-// The quick way; false where it cannot tell.
+// The quick way as far as the few that are left; their number, or 0 where it cannot tell.
 template <int NE>
-__device__ __forceinline__ bool route_quickly(const RouteParams& p, Token& tok, float* members, uint32_t* mine) {
+__device__ __forceinline__ int rule_out(const RouteParams& p, Token& tok, float* members, Few& few) {
     const int lane = threadIdx.x & 63, E = p.E, e0 = lane * NE;
     const int64_t t = tok.t;
 
@@ -338,9 +351,9 @@ __device__ __forceinline__ bool route_quickly(const RouteParams& p, Token& tok, 
         all = c[0];
 #pragma unroll
         for (int i = 1; i < NE; ++i) all += c[i];
-        if (__ballot(all != all)) return false;
+        if (__ballot(all != all)) return 0;
     } else if (odd) {
-        return false;
+        return 0;
     }
 
     if (p.groups > 1) {
@@ -434,22 +447,26 @@ __device__ __forceinline__ bool route_quickly(const RouteParams& p, Token& tok, 
         before = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, before));
         total += __popcll(m);
     }
-    if (total > 64) return false;
-    // a lane each, in the experts' order
+    if (total > 64) return 0;
 #pragma unroll
     for (int i = 0; i < NE; ++i)
         if (key[i] >= bar) {
-            mine[before] = (uint32_t)(e0 + i);
-            mine[64 + before] = __float_as_uint(l[i]);
-            if (p.bias) mine[128 + before] = __float_as_uint(bias[i]);
+            few.expert[before] = (uint32_t)(e0 + i);
+            few.logit[before] = l[i];
+            if (p.bias) few.bias[before] = bias[i];
             ++before;
         }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    const int e = (int)mine[lane];
-    const float x = __uint_as_float(mine[64 + lane]);
+    return total;
+}
+
+// ... and their order: the value of each in 64 bits, its rank by counting the larger ones; of
+// equal upper halves the lower count too.  Lane by lane of the wave, `total` of them, ...
+__device__ __forceinline__ void rank_few(const Token& tok, const Few& few, int total) {
+    const RouteParams& p = tok.p;
+    const int lane = threadIdx.x & 63;
+    const float x = few.logit[lane];
     const double s = tok.score(x) * tok.inv;
-    const uint64_t full = p.bias ? ordered(s + (double)__uint_as_float(mine[128 + lane])) : (uint64_t)ordered(x) << 32;
+    const uint64_t full = p.bias ? ordered(s + (double)few.bias[lane]) : (uint64_t)ordered(x) << 32;
     const uint32_t k = lane < total ? (uint32_t)(full >> 32) : 0;  // (0: below every value's)
     int rank = 0;
     uint64_t equal = 0;  // lanes that have another's upper half
@@ -466,18 +483,71 @@ __device__ __forceinline__ bool route_quickly(const RouteParams& p, Token& tok, 
             rank += o > full || (o == full && j < lane) ? 1 : 0;
         }
     }
-    tok.store(lane < total && rank < p.k, s, e, rank, total <= 16);
-    return true;
+    tok.store(lane < total && rank < p.k, s, (int)few.expert[lane], rank);
+}
+// ... or, where a token has up to 16, four tokens in one wave, 16 lanes each: the others of a row
+// come by its rotation.
+template <int N>
+__device__ __forceinline__ void compare(uint64_t full, bool whole, int lane, int& rank, bool& equal) {
+    const uint32_t hi = (uint32_t)(full >> 32), lo = (uint32_t)full, o_hi = dpp<0x120 + N>(hi);  // row_ror:N
+    if (whole) {
+        const uint64_t o = (uint64_t)o_hi << 32 | dpp<0x120 + N>(lo);
+        rank += o > full || (o == full && ((lane - N) & 15) < (lane & 15)) ? 1 : 0;
+    } else {
+        rank += o_hi > hi ? 1 : 0;
+        equal = equal || o_hi == hi;
+    }
+    if constexpr (N < 15) compare<N + 1>(full, whole, lane, rank, equal);
+}
+__device__ __forceinline__ void rank_rows(const RouteParams& p, int64_t first, const Few (&few)[4]) {
+    const int lane = threadIdx.x & 63, w = lane >> 4, i = lane & 15;
+    const Few& f = few[w];
+    const int total = f.count;
+    const Token tok{p, first + w, f.top, f.inv};
+    const float x = f.logit[i];
+    const double s = tok.score(x) * tok.inv;
+    uint64_t full = p.bias ? ordered(s + (double)f.bias[i]) : (uint64_t)ordered(x) << 32;
+    full = i < total ? full : (uint64_t)i;  // (below every value's, and different)
+    int rank = 0;
+    bool equal = false;
+    compare<1>(full, false, lane, rank, equal);
+    if (__ballot(equal && i < total)) {
+        rank = 0;
+        compare<1>(full, true, lane, rank, equal);
+    }
+    tok.store<true>(i < total && rank < p.k, s, (int)f.expert[i], rank);
 }
 
+// A wave to a token as far as the few; then one wave for the four tokens of a workgroup (which
+// one goes round, so that no SIMD has them all): ranking and weights in 64 bits are a third of
+// the instructions, and a token's few fill a quarter of a wave.  16384 tokens, 256 experts in
+// 8 groups, biased sigmoid scores: 13.7 us, each wave to the end for its own token 16.4; what
+// is left is the vector instructions' issue (some 340 a token, 9 us) and the launch.
 template <int NE>
 __global__ __launch_bounds__(256) void route_kernel(RouteParams p) {
     extern __shared__ float members[];  // [4 waves][E], for groups that do not fill whole lanes
-    __shared__ uint32_t picked[4][3 * 64];  // each wave's few: expert, logit, bias
+    __shared__ Few few[4];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Token tok{p, (int64_t)blockIdx.x * 4 + wave, 0.f, 1.0};
-    if (tok.t >= p.T) return;  // whole waves; no barrier in what follows
-    if (!route_quickly<NE>(p, tok, members + (int64_t)wave * p.E, picked[wave])) route_slowly(tok);
+    int total = 0;
+    if (tok.t < p.T) {
+        total = rule_out<NE>(p, tok, members + (int64_t)wave * p.E, few[wave]);
+        if (total == 0) {
+            route_slowly(tok);
+        } else if (total > 16) {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            rank_few(tok, few[wave], total);
+            total = 0;
+        }
+    }
+    if ((threadIdx.x & 63) == 0) {
+        few[wave].count = total;
+        few[wave].top = tok.top;
+        few[wave].inv = tok.inv;
+    }
+    __syncthreads();
+    if (wave == (int)(blockIdx.x & 3)) rank_rows(p, (int64_t)blockIdx.x * 4, few);
 }
 
 template <int NE>
