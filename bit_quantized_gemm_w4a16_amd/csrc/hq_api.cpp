@@ -7,6 +7,7 @@
 // ahead of time.  The host path does O(1) checks and no allocation, in the
 // spirit of the launch-overhead work in "Humming v0.1.0-0.1.4", section
 // "v0.1.1".
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -606,8 +607,9 @@ hq_status hq_workspace_bytes(const hq_layer_desc* desc, int64_t M_or_T, int32_t 
     if (M_or_T < 0 || M_or_T > (1LL << 30)) return set_error(HQ_ERR_INVALID_ARG, "M/T out of range");
     if (desc->num_experts) {
         if (top_k < 1 || top_k > desc->num_experts) return set_error(HQ_ERR_INVALID_ARG, "top_k out of range");
-        *bytes = L.kind == Kind::FP8_BLOCK ? moe_f8_workspace(M_or_T, top_k, desc->num_experts)
-                                           : moe_layout(M_or_T, top_k, desc->num_experts, true).bytes;  // Indexed needs the most
+        // Indexed needs the most; and what hq_moe_align needs fits in any layer's
+        *bytes = L.kind == Kind::FP8_BLOCK ? std::max(moe_f8_workspace(M_or_T, top_k, desc->num_experts), moe_align_workspace(M_or_T, top_k, desc->num_experts))
+                                           : moe_layout(M_or_T, top_k, desc->num_experts, true).bytes;
     } else {
         *bytes = dense_workspace(L, M_or_T);
     }

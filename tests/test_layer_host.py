@@ -172,3 +172,13 @@ def test_norm_and_swiglu_definitions_by_hand():
     np.testing.assert_array_equal(ol.scales(np.array([[0.0, 0.0, 8.0, np.nan]]), 2, 4.0), [[1.0, 2.0]])
     np.testing.assert_array_equal(ol.step_e4m3(np.array([0.0, 1.0, 1.9, 2.0, 448.0, 2.0 ** -7])), [2.0 ** -9, 0.125, 0.125, 0.25, 32.0, 2.0 ** -9])
     np.testing.assert_array_equal(ol.step_e2m1(np.array([0.2, 1.0, 2.0, 4.0, 6.0])), [0.5, 0.5, 1.0, 2.0, 2.0])
+
+
+@pytest.mark.parametrize("T,top_k,E", [(1, 1, 1), (7, 4, 16), (8, 8, 256), (9, 8, 256), (100, 2, 4096), (512, 8, 256), (5000, 8, 32), (65536, 8, 256)])
+def test_a_layers_workspace_holds_the_sorting_of_its_routes(T, top_k, E):
+    """hq_moe_align takes the workspace of a layer with the same T and top_k (past the check of its size the address is refused)."""
+    for desc in (hq.desc_moe_fp8_blockwise(E, 256, 256), hq.desc_moe_mxfp4(E, 256, 256)):
+        n = hq.hq_workspace_bytes(desc, T, top_k)
+        with pytest.raises(hq.HQError) as e:
+            hq.hq_moe_align(T, top_k, E, A, A, A, A + 4, n, stream=0)
+        assert e.value.status == hq.HQ_ERR_ALIGNMENT
