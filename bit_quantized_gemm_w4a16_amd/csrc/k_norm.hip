@@ -355,10 +355,14 @@ hipError_t go(const RowParams& p, hipStream_t st) {
 // Threads of a row by its width.  One wave as long as its registers hold the row: no barrier
 // for the sums (8191 rows, norm with a residual and scales of tokens, us: width 512 one wave
 // 9.8, four 14.3; 1024 12.5, 19.1; 2048 21.6, 26.1), but SwiGLU, which has less to wait for and
-// twice the input, from 1024 on four (2048: 19.4, 17.3).  Then four or sixteen (4096: four
+// twice the input, from 1024 on four (2048: 19.4, 17.3).  Then four, eight or sixteen (4096: four
 // 46.6, eight 54.8; 8192 four 85.7, eight 85.1, sixteen with a group each 1.5 times as long;
-// 16384 four 178, eight 169, sixteen 171; SwiGLU 135, 138, 128).  For 300 rows none differ
-// by more than the launch does, but at 16384: 12.3, 10.5, 10.7.
+// 16384 four 178, eight 169, sixteen 171; SwiGLU 135, 138, 128).  Up to kFewRows rows the
+// steps of a thread count, so it has as few groups as there is a variant for (norm with scales
+// of blocks, on the card, 5 / 256 / 700 rows: 2048 one wave 5.1 / 6.0 / 6.4, four 3.2 / 3.7 /
+// 4.4; 4096 four 4.1 / 4.6 / 6.3, eight 3.4 / 4.1 / 6.2; 8192 four 5.5 / 6.6 / 9.9, eight 4.2 /
+// 5.4 / 9.4, sixteen 3.9 / 5.2 / 9.4).
+constexpr int64_t kFewRows = 1024;
 template <bool BF16, Quant Q>
 hipError_t pick(const RowParams& p, bool vec, hipStream_t st) {
     const int K = p.width;
@@ -367,15 +371,16 @@ hipError_t pick(const RowParams& p, bool vec, hipStream_t st) {
         // 2-byte loads that are consecutive over a wave 48)
         if (!vec) {
             if (K <= 2048) return go<BF16, Q, 64, 4, false>(p, st);
-            if (K <= 8192) return go<BF16, Q, 256, 4, false>(p, st);
+            if (K <= 8192) return go<BF16, Q, 512, 2, false>(p, st);
             return go<BF16, Q, 1024, 8, false>(p, st);
         }
     }
+    const bool few = p.rows <= kFewRows;
     if (K <= 512) return go<BF16, Q, 64, 1, true>(p, st);
-    if (K <= 1024) return go<BF16, Q, 64, 2, true>(p, st);
-    if (K <= 2048) return p.silu ? go<BF16, Q, 256, 1, true>(p, st) : go<BF16, Q, 64, 4, true>(p, st);
-    if (K <= 4096) return go<BF16, Q, 256, 2, true>(p, st);
-    if (K <= 8192) return go<BF16, Q, 256, 4, true>(p, st);
+    if (K <= 1024 && !few) return go<BF16, Q, 64, 2, true>(p, st);
+    if (K <= 2048) return p.silu || few ? go<BF16, Q, 256, 1, true>(p, st) : go<BF16, Q, 64, 4, true>(p, st);
+    if (K <= 4096) return few ? go<BF16, Q, 512, 1, true>(p, st) : go<BF16, Q, 256, 2, true>(p, st);
+    if (K <= 8192) return go<BF16, Q, 512, 2, true>(p, st);
     if (K <= 16384) return go<BF16, Q, 1024, 2, true>(p, st);
     return go<BF16, Q, 1024, 8, true>(p, st);
 }

@@ -7,7 +7,7 @@ import torch
 import synthetic as syn
 from bit_quantized_gemm_w4a16_amd import hq
 from gpu_util import note
-from layer_util import DT, FORMS, SILU_DELTA, check_rows, f64, outputs, run_norm
+from layer_util import DT, FORMS, NORM_DELTA, SILU_DELTA, check_rows, f64, outputs, run_norm
 from oracle import layer as ol
 from test_gpu_moe_f8 import Experts, both_ways
 from test_gpu_route import check, logits_of, summed
@@ -250,3 +250,26 @@ def test_experts_on_two_streams():
     torch.cuda.synchronize()
     for *_, want, out, ws, st in jobs:
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M", [1024, 1025])
+@pytest.mark.parametrize("form,K", [(f, k) for f in FORMS for k in (512, 640, 1024, 1152, 2048, 2176, 4096, 4224)] + [(f, k) for f in ("same", "f8_token") for k in (1999, 4001)])
+def test_norm_rows_where_the_threads_of_a_row_change(form, K, M):
+    note(f"norm {form} {M} x {K}")
+    g = torch.Generator().manual_seed(K)
+    x, r = (torch.randn(M, K, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    w = (1 + 0.2 * torch.randn(K, generator=g)).cuda()
+    total = torch.empty_like(x)
+    got = run_norm(form, "bf16", x, r, w, M, K, sum_out=total, offset=0.5)
+    h, y = ol.rms_norm(f64(x), f64(r), f64(w), float(np.float32(1e-6)), 0.5)
+    check_rows(form, "bf16", y, 2 * NORM_DELTA, *got)
+    assert (np.abs(f64(total) - h) <= np.abs(h) * (2.0 ** -8 + 2.0 ** -23)).all()
+
+
+@pytest.mark.parametrize("rows", [1024, 1025])
+@pytest.mark.parametrize("I", [512, 1024, 2048, 4096])
+def test_swiglu_rows_where_the_threads_of_a_row_change(rows, I):
+    note(f"swiglu {rows} x {I}")
+    gu = (1.5 * torch.randn(rows, 2 * I, generator=torch.Generator().manual_seed(I))).to(torch.bfloat16).cuda()
+    for form in ("f8_token", "mx_f8"):
+        check_rows(form, "bf16", ol.silu_mul(f64(gu)), SILU_DELTA, *swiglu(form, "bf16", gu, rows, I))
