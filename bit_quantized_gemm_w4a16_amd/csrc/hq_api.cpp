@@ -850,7 +850,7 @@ hq_status hq_rmsnorm(const hq_norm_desc* d, int64_t M, int64_t K, const void* x,
         return set_error(HQ_ERR_UNSUPPORTED, "norm weight dtype %d (that of x, or FP32)", d->weight_dtype);
     if (!(d->eps >= 0.f) || !std::isfinite(d->eps) || !std::isfinite(d->weight_offset))
         return set_error(HQ_ERR_INVALID_ARG, "eps must be 0 or positive, weight_offset finite");
-    if (M < 0 || M > (1LL << 22) || K < 1) return set_error(HQ_ERR_INVALID_ARG, "M=%lld K=%lld out of range", (long long)M, (long long)K);
+    if (M < 0 || M >= (1LL << 22) || K < 1) return set_error(HQ_ERR_INVALID_ARG, "M=%lld K=%lld out of range", (long long)M, (long long)K);
     if (K > kRowMaxWidth) return set_error(HQ_ERR_UNSUPPORTED, "rows of at most %d elements are built", kRowMaxWidth);
     RowArgs a{};
     const hq_status st = row_out(d->dtype, d->out_dtype, d->a_scale, K, &a.kind);
@@ -890,7 +890,7 @@ hq_status hq_rmsnorm(const hq_norm_desc* d, int64_t M, int64_t K, const void* x,
 hq_status hq_silu_mul_quant(int32_t dtype, int32_t out_dtype, int32_t a_scale, int64_t rows, int64_t I, const void* gate_up, void* out,
                             void* out_scale, hq_stream_t stream) {
     if (dtype != HQ_DT_BF16 && dtype != HQ_DT_FP16) return set_error(HQ_ERR_UNSUPPORTED, "dtype %d (BF16 or FP16)", dtype);
-    if (rows < 0 || rows > (1LL << 22) || I < 8 || I % 8)
+    if (rows < 0 || rows >= (1LL << 22) || I < 8 || I % 8)
         return set_error(HQ_ERR_INVALID_ARG, "rows=%lld I=%lld out of range (I a multiple of 8)", (long long)rows, (long long)I);
     if (I > kRowMaxWidth) return set_error(HQ_ERR_UNSUPPORTED, "rows of at most %d elements are built", kRowMaxWidth);
     RowArgs a{};

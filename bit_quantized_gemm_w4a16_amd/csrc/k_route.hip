@@ -748,7 +748,8 @@ hipError_t combine_launch(const CombineArgs& a) {
     // a workgroup for a token, of as many threads as share its columns evenly; for few
     // tokens, which do not fill the chip, one for each 128 threads' columns (7168 columns, 5
     // tokens: 3.2 us, one workgroup each 4.6; 60: 3.7, 4.9)
-    const int64_t units = vec ? a.N / 8 : a.N, turns = ceil_div(units, 512);
+    // (workgroups times threads stay below 2^32)
+    const int64_t units = vec ? a.N / 8 : a.N, turns = ceil_div(units, a.T < 1 << 23 ? 512 : 256);
     const int threads = a.T < 64 ? 128 : (int)ceil_div(ceil_div(units, turns), 64) * 64;
     const dim3 grid((unsigned)a.T, (unsigned)(a.T < 64 ? ceil_div(units, threads) : 1)), block(threads);
     // Rows that the 256 MB behind the L2s cannot hold go past them (y of 470 MB: 99 us, loaded

@@ -432,8 +432,8 @@ hq_status hq_gemm_plan(const hq_layer_desc* desc, int64_t M, char* buf, size_t l
  * [rows of A][K/128]; their sums over K go block by block in order, in fp32, so a
  * row's result does not depend on the other rows.  (As in every product of 8-bit
  * floats here, the matrix instruction adds the products of 8 neighbouring K at 13 bits
- * below the largest's power of two: about 2^-19 of the sum of absolute values.)  Rows of D whose id is outside
- * 0..num_experts-1 are not written.
+ * below the largest's power of two: about 2^-19 of the sum of absolute values.)  Rows
+ * of D whose id is outside 0..num_experts-1 are not written.
  */
 hq_status hq_moe_gemm(const hq_layer_desc* desc, int32_t mode, int64_t T, int32_t top_k,
                       const void* A, const float* a_scale, const int32_t* topk_ids,
@@ -547,7 +547,7 @@ hq_status hq_moe_gather(int32_t dtype, int64_t T, int32_t top_k, int64_t K, cons
  *   weight       [K], weight_dtype: dtype or FP32
  *   sum_out      dtype, or NULL; may be x or residual itself with the same stride
  *   out          dense [M][K] (E2M1: [M][K/2] bytes); out_scale as the table says
- * K 1..65536, M at most 2^22.  Rows and strides that are multiples of 8 are read 16
+ * K 1..65536, M below 2^22.  Rows and strides that are multiples of 8 are read 16
  * bytes at a time; others are taken too, but not with block scales (128 or MX).
  * Squares are summed in fp32: a row whose squares pass 2^127 in sum gives zeros (NaN
  * where h is infinite).  Apart from sum_out the outputs must not overlap the inputs.
@@ -570,7 +570,7 @@ hq_status hq_rmsnorm(const hq_norm_desc* desc, int64_t M, int64_t K, const void*
  * SwiGLU with a quantised output: y = silu(gate) * up of rows gate | up ([rows][2I],
  * dtype BF16 or FP16), fp32 as in hq_silu_mul, and y's codes and scales in any of
  * the quantised forms of hq_rmsnorm.  I a multiple of 8 (of 128 or 32 for block
- * scales), at most 65536; rows at most 2^22; the buffers must not overlap.
+ * scales), at most 65536; rows below 2^22; the buffers must not overlap.
  */
 hq_status hq_silu_mul_quant(int32_t dtype, int32_t out_dtype, int32_t a_scale, int64_t rows, int64_t I, const void* gate_up,
                             void* out, void* out_scale, hq_stream_t stream);

@@ -182,3 +182,10 @@ def test_a_layers_workspace_holds_the_sorting_of_its_routes(T, top_k, E):
         with pytest.raises(hq.HQError) as e:
             hq.hq_moe_align(T, top_k, E, A, A, A, A + 4, n, stream=0)
         assert e.value.status == hq.HQ_ERR_ALIGNMENT
+
+
+def test_as_many_rows_as_a_launch_holds():
+    """Workgroups times threads stay below 2^32, with up to 1024 threads a row."""
+    for M, want in ((1 << 22, BAD), ((1 << 22) - 1, ALIGN)):
+        assert status_of(hq.hq_rmsnorm, norm(), **{**NORM, "M": M, "x": A + 8}) == want
+        assert status_of(hq.hq_silu_mul_quant, **{**SILU, "rows": M, "gate_up": A + 8}) == want
