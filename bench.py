@@ -908,7 +908,8 @@ def tune_table(work, log_fn=log):
 # paged-cache operators and of a routed layer's, and not hq_api.cpp and hq.h, which
 # choose the launches: a figure names its launch, and counts only where that is
 # still the one planned.
-OTHER_SOURCES = ("k_attn.hip", "k_kv.hip", "hq_kv.h", "k_norm.hip", "k_route.hip", "k_moe_f8.hip", "hq_layer.h", "hq_api.cpp")
+OTHER_SOURCES = ("k_attn.hip", "k_kv.hip", "hq_kv.h", "k_norm.hip", "k_route.hip", "k_moe_f8.hip", "hq_layer.h", "layer_rows.hpp",
+                 "hq_api.cpp")
 KERNEL_SOURCES = sorted("bit_quantized_gemm_w4a16_amd/csrc/" + f
                         for f in os.listdir(os.path.join(ROOT, "bit_quantized_gemm_w4a16_amd", "csrc"))
                         if f.endswith((".hip", ".hpp", ".h", ".cpp")) and f not in OTHER_SOURCES)

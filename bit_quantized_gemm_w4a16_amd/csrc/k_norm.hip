@@ -17,6 +17,7 @@
 // in tokens, 86 and now 76 (5.4 TB/s).  A call of few rows takes as long as its launch.
 #include "hq_device.hpp"
 #include "hq_layer.h"
+#include "layer_rows.hpp"
 
 namespace hq {
 
@@ -115,54 +116,9 @@ __device__ __forceinline__ uint32_t e2m1_of(float x, float v) {
     return mag | ((__float_as_uint(x) >> 28) & 8u);
 }
 
-template <bool BF16>
-__device__ __forceinline__ void unpack8(v4u v, float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t u = v[i];
-        f[2 * i] = bits16_to_f32<BF16>((uint16_t)u);
-        f[2 * i + 1] = bits16_to_f32<BF16>((uint16_t)(u >> 16));
-    }
-}
-template <bool BF16>
-__device__ __forceinline__ v4u pack8(const float (&f)[8]) {
-    v4u v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (uint32_t)f32_to_16<BF16>(f[2 * i]) | ((uint32_t)f32_to_16<BF16>(f[2 * i + 1]) << 16);
-    return v;
-}
-
-// Eight 16-bit elements at `at`, of which n are the row's (the others read as 0).  VEC: the
-// address is a multiple of 16 and n is 8 or less than 1.  Without it rows start at any element: the same
-// wide access, which the memory takes at any alignment, and the row's last group by elements.
-struct __attribute__((packed, aligned(2))) Any16 {
-    v4u v;
-};
 struct __attribute__((packed, aligned(1))) Any8 {
     uint2 v;
 };
-template <bool VEC>
-__device__ __forceinline__ v4u load8(const uint16_t* at, int n) {
-    if (n >= 8) return VEC ? ld16(at) : ((const Any16*)at)->v;
-    v4u v{0, 0, 0, 0};
-    if constexpr (!VEC) {
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (i < n) v[i >> 1] |= (uint32_t)at[i] << (16 * (i & 1));
-    }
-    return v;
-}
-template <bool VEC>
-__device__ __forceinline__ void store8(uint16_t* at, v4u v, int n) {
-    if (n >= 8) {
-        if constexpr (VEC) *(v4u*)at = v;
-        else ((Any16*)at)->v = v;
-    } else if constexpr (!VEC) {
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (i < n) at[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
-    }
-}
 
 // Sum or maximum over the TPR threads of a row (TPR 64: one wave; else the whole workgroup).
 template <int TPR, bool MAX>
@@ -355,7 +311,8 @@ hipError_t go(const RowParams& p, hipStream_t st) {
 // Threads of a row by its width.  One wave as long as its registers hold the row: no barrier
 // for the sums (8191 rows, norm with a residual and scales of tokens, us: width 512 one wave
 // 9.8, four 14.3; 1024 12.5, 19.1; 2048 21.6, 26.1), but SwiGLU, which has less to wait for and
-// twice the input, from 1024 on four (2048: 19.4, 17.3).  Then four, eight or sixteen (4096: four
+// twice the input, from 1024 on four (2048, scales of blocks: 19.4, 17.3) unless it waits for a
+// row's scale too (tokens: 18.2, 24.8).  Then four, eight or sixteen (4096: four
 // 46.6, eight 54.8; 8192 four 85.7, eight 85.1, sixteen with a group each 1.5 times as long;
 // 16384 four 178, eight 169, sixteen 171; SwiGLU 135, 138, 128).  Up to kFewRows rows the
 // steps of a thread count, so it has as few groups as there is a variant for (norm with scales
@@ -378,7 +335,7 @@ hipError_t pick(const RowParams& p, bool vec, hipStream_t st) {
     const bool few = p.rows <= kFewRows;
     if (K <= 512) return go<BF16, Q, 64, 1, true>(p, st);
     if (K <= 1024 && !few) return go<BF16, Q, 64, 2, true>(p, st);
-    if (K <= 2048) return p.silu || few ? go<BF16, Q, 256, 1, true>(p, st) : go<BF16, Q, 64, 4, true>(p, st);
+    if (K <= 2048) return (p.silu && Q != Quant::TOKEN) || few ? go<BF16, Q, 256, 1, true>(p, st) : go<BF16, Q, 64, 4, true>(p, st);
     if (K <= 4096) return few ? go<BF16, Q, 512, 1, true>(p, st) : go<BF16, Q, 256, 2, true>(p, st);
     if (K <= 8192) return go<BF16, Q, 512, 2, true>(p, st);
     if (K <= 16384) return go<BF16, Q, 1024, 2, true>(p, st);

@@ -18,6 +18,7 @@
 #include "hq_device.hpp"
 #include "hq_kv.h"
 #include "hq_layer.h"
+#include "layer_rows.hpp"
 
 namespace hq {
 
@@ -591,11 +592,12 @@ struct CombineParams {
 // out[t] = rnd16(add[t] + sum_j w[t][j] y[row(t, j)]), j in order, fp32.  Bound by HBM, so
 // what matters is how many loads are on their way: a workgroup takes a token, its lanes
 // look up the token's rows side by side, and a thread then has the loads of eight rows
-// under way at a time (8 columns each, VEC: 16 bytes).  A row of weight 0 is not read.
+// under way at a time, 8 columns each (of which `cols` are the row's).  A row of weight 0 is
+// not read.  4095 tokens of 8 rows, us: 7168 columns 99 (5.9 TB/s), 7169 120, 1776 26.7, 1777
+// 34.2 (by single columns 45.4).
 template <bool BF16, bool VEC, bool NT, int R>
-__device__ __forceinline__ void add_rows(const CombineParams& p, uint64_t& left, int64_t row, float w, int64_t n, float (&acc)[VEC ? 8 : 1]) {
+__device__ __forceinline__ void add_rows(const CombineParams& p, uint64_t& left, int64_t row, float w, int64_t n, int cols, float (&acc)[8]) {
     v4u v[R];
-    uint32_t one[R];
     float wj[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {  // the next R rows that count
@@ -603,28 +605,20 @@ __device__ __forceinline__ void add_rows(const CombineParams& p, uint64_t& left,
         left &= left - 1;
         const int64_t at = (int64_t)__builtin_amdgcn_readlane((int)row, j);
         wj[r] = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(w), j));
-        if constexpr (VEC && NT) v[r] = ld_nt((const v4u*)(p.y + at * p.N + n));
-        else if constexpr (VEC) v[r] = ld16(p.y + at * p.N + n);
-        else one[r] = p.y[at * p.N + n];
+        v[r] = load8<VEC, NT>(p.y + at * p.N + n, cols);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        if constexpr (VEC) {
+        float y[8];
+        unpack8<BF16>(v[r], y);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t u = v[r][i];
-                acc[2 * i] += wj[r] * bits16_to_f32<BF16>((uint16_t)u);
-                acc[2 * i + 1] += wj[r] * bits16_to_f32<BF16>((uint16_t)(u >> 16));
-            }
-        } else {
-            acc[0] += wj[r] * bits16_to_f32<BF16>((uint16_t)one[r]);
-        }
+        for (int i = 0; i < 8; ++i) acc[i] += wj[r] * y[i];
     }
 }
 
 template <bool BF16, bool VEC, bool NT>
 __global__ __launch_bounds__(512) void combine_kernel(CombineParams p) {
-    constexpr int C = VEC ? 8 : 1;
+    constexpr int C = 8;
     __shared__ int row_of[kCombineFew];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63;
@@ -664,35 +658,22 @@ __global__ __launch_bounds__(512) void combine_kernel(CombineParams p) {
         const int64_t n = (n0 + threadIdx.x) * C;
         const bool live = n < p.N;
         const int64_t nl = live ? n : 0;  // (past the row: its start, not stored)
-        v4u a = v4u{0, 0, 0, 0};
-        uint32_t a1 = 0;
-        if (p.add) {
-            if constexpr (VEC) a = ld16(p.add + t * p.N + nl);
-            else a1 = p.add[t * p.N + nl];
-        }
-        float acc[C] = {};
+        const int cols = VEC ? 8 : (int)min(p.N - nl, (int64_t)8);
+        float a[8], acc[8] = {};
+        unpack8<BF16>(p.add ? load8<VEC>(p.add + t * p.N + nl, cols) : v4u{0, 0, 0, 0}, a);
         for (int j0 = 0; j0 < p.k; j0 += 64) {
             float w = w0;
             int64_t row = row0;
             uint64_t left = j0 ? look(j0, w, row) : have0;
-            while (__popcll(left) >= 8) add_rows<BF16, VEC, NT, 8>(p, left, row, w, nl, acc);
-            if (__popcll(left) >= 4) add_rows<BF16, VEC, NT, 4>(p, left, row, w, nl, acc);
-            if (__popcll(left) >= 2) add_rows<BF16, VEC, NT, 2>(p, left, row, w, nl, acc);
-            if (left) add_rows<BF16, VEC, NT, 1>(p, left, row, w, nl, acc);
+            while (__popcll(left) >= 8) add_rows<BF16, VEC, NT, 8>(p, left, row, w, nl, cols, acc);
+            if (__popcll(left) >= 4) add_rows<BF16, VEC, NT, 4>(p, left, row, w, nl, cols, acc);
+            if (__popcll(left) >= 2) add_rows<BF16, VEC, NT, 2>(p, left, row, w, nl, cols, acc);
+            if (left) add_rows<BF16, VEC, NT, 1>(p, left, row, w, nl, cols, acc);
         }
         if (!live) continue;
-        if constexpr (VEC) {
-            v4u o;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t u = a[i];
-                const float x = acc[2 * i] + bits16_to_f32<BF16>((uint16_t)u), y = acc[2 * i + 1] + bits16_to_f32<BF16>((uint16_t)(u >> 16));
-                o[i] = (uint32_t)f32_to_16<BF16>(x) | ((uint32_t)f32_to_16<BF16>(y) << 16);
-            }
-            *(v4u*)(p.out + t * p.N + n) = o;
-        } else {
-            p.out[t * p.N + n] = f32_to_16<BF16>(acc[0] + bits16_to_f32<BF16>((uint16_t)a1));
-        }
+        for (int i = 0; i < 8; ++i) acc[i] += a[i];
+        store8<VEC>(p.out + t * p.N + n, pack8<BF16>(acc), cols);
     }
 }
 
@@ -749,18 +730,17 @@ hipError_t combine_launch(const CombineArgs& a) {
     // tokens, which do not fill the chip, one for each 128 threads' columns (7168 columns, 5
     // tokens: 3.2 us, one workgroup each 4.6; 60: 3.7, 4.9)
     // (workgroups times threads stay below 2^32)
-    const int64_t units = vec ? a.N / 8 : a.N, turns = ceil_div(units, a.T < 1 << 23 ? 512 : 256);
+    const int64_t units = ceil_div(a.N, 8), turns = ceil_div(units, a.T < 1 << 23 ? 512 : 256);
     const int threads = a.T < 64 ? 128 : (int)ceil_div(ceil_div(units, turns), 64) * 64;
     const dim3 grid((unsigned)a.T, (unsigned)(a.T < 64 ? ceil_div(units, threads) : 1)), block(threads);
     // Rows that the 256 MB behind the L2s cannot hold go past them (y of 470 MB: 99 us, loaded
     // as others are 122; of 115 MB, just written: 29, 26)
     const bool nt = P * a.N * 2 > (int64_t)256 << 20;
-    if (vec && a.bf16 && nt) hipLaunchKernelGGL((combine_kernel<true, true, true>), grid, block, 0, a.stream, p);
-    else if (vec && a.bf16) hipLaunchKernelGGL((combine_kernel<true, true, false>), grid, block, 0, a.stream, p);
-    else if (vec && nt) hipLaunchKernelGGL((combine_kernel<false, true, true>), grid, block, 0, a.stream, p);
-    else if (vec) hipLaunchKernelGGL((combine_kernel<false, true, false>), grid, block, 0, a.stream, p);
-    else if (a.bf16) hipLaunchKernelGGL((combine_kernel<true, false, false>), grid, block, 0, a.stream, p);
-    else hipLaunchKernelGGL((combine_kernel<false, false, false>), grid, block, 0, a.stream, p);
+    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, a.stream, p); };
+    if (a.bf16 && vec) launch(nt ? combine_kernel<true, true, true> : combine_kernel<true, true, false>);
+    else if (a.bf16) launch(nt ? combine_kernel<true, false, true> : combine_kernel<true, false, false>);
+    else if (vec) launch(nt ? combine_kernel<false, true, true> : combine_kernel<false, true, false>);
+    else launch(nt ? combine_kernel<false, false, true> : combine_kernel<false, false, false>);
     return hipGetLastError();
 }
 

@@ -547,8 +547,8 @@ hq_status hq_moe_gather(int32_t dtype, int64_t T, int32_t top_k, int64_t K, cons
  *   weight       [K], weight_dtype: dtype or FP32
  *   sum_out      dtype, or NULL; may be x or residual itself with the same stride
  *   out          dense [M][K] (E2M1: [M][K/2] bytes); out_scale as the table says
- * K 1..65536, M below 2^22.  Rows and strides that are multiples of 8 are read 16
- * bytes at a time; others are taken too, but not with block scales (128 or MX).
+ * K 1..65536, M below 2^22.  Rows and strides that are multiples of 8 are the
+ * fastest; others are taken too, but not with block scales (128 or MX).
  * Squares are summed in fp32: a row whose squares pass 2^127 in sum gives zeros (NaN
  * where h is infinite).  Apart from sum_out the outputs must not overlap the inputs.
  */
@@ -620,7 +620,7 @@ hq_status hq_moe_route(const hq_route_desc* desc, int64_t T, const void* logits,
  * A row whose weight is 0 is not read and adds nothing, whatever it holds; nor does a
  * pair that sorted_pairs does not name (one named twice has either row).  workspace:
  * T*top_k*4 bytes with sorted_pairs, else none.  N 1..2^21, T at most 2^23; rows of a
- * multiple of 8 elements are read 16 bytes at a time.
+ * multiple of 8 elements are the fastest.
  */
 hq_status hq_moe_combine(int32_t dtype, int64_t T, int32_t top_k, int64_t N, const void* y, const float* topk_weights,
                          const int32_t* sorted_pairs, const void* add, void* out, void* workspace, size_t ws_bytes,

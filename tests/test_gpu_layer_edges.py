@@ -103,7 +103,7 @@ def test_route_past_31_bits():
     assert torch.equal(ids.view(-1, 50, 8), want.expand(T // 50, 50, 8)) and torch.equal(w.view(-1, 50, 8), ww.expand(T // 50, 50, 8))
 
 
-@pytest.mark.parametrize("T,k,N", [(4200, 5, 7168), (15100, 20, 7168)])
+@pytest.mark.parametrize("T,k,N", [(4200, 5, 7168), (4200, 5, 7171), (15100, 20, 7168)])
 @pytest.mark.parametrize("ordered", [False, True])
 def test_combine_past_the_cache_and_31_bits(T, k, N, ordered):
     note(f"combine T={T} k={k} N={N} sorted={ordered}")
