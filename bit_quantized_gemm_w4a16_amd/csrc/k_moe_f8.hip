@@ -31,6 +31,7 @@ namespace {
 constexpr int kF8InlineP = 64;   // one pair per lane of a wave
 constexpr int kF8Chunk = 4096;   // pairs of one routing workgroup
 constexpr int kF8TileRows = 256; // rows of a large m-tile, at most
+constexpr int kF8LeastRows = 96; // (fewer take as long)
 constexpr int kF8Rows = 32;      // rows that the weight stream takes at a time
 // Which experts the weight stream takes: those of up to kF8Rows rows where experts have
 // up to kF8Mean rows in the mean, else none.  Two launches of which each has a part of the
@@ -52,24 +53,37 @@ struct Tile {
 
 struct F8Layout {  // byte offsets into the workspace
     size_t hist, sorted, tiles[2], ntiles, bytes;
-    int stream;            // as in F8Lists
+    int stream, tile_rows;  // as in F8Lists
     int64_t max_tiles[2];  // bounds of the lists of the weight stream's m-tiles and of the others
 };
 struct F8Lists {
-    int stream;  // experts of up to so many rows are for the weight stream (0: none)
+    int stream;     // experts of up to so many rows are for the weight stream (0: none)
+    int tile_rows;  // of a larger m-tile, at most
     Tile* tiles[2];
     int* ntiles;  // [2]
     int max_tiles[2];
 };
 
-F8Layout f8_layout(int64_t T, int top_k, int E) {
+// Rows of the large m-tiles: as few as leave all tiles, by the experts' mean, one for each CU.
+// (96 rows or 256, us: 1000 rows on 2 experts of 2048 x 7168 51, 85; 512 on one of 4096 x 4096 32,
+// 54; 4096 on one of 1024 x 2048 24, 37; but 3460 on 2 of 4096 x 640, where 96 make 576 tiles, 30, 23.)
+int f8_rows_of_tiles(int64_t P, int64_t held, int64_t N) {
+    int rows = kF8LeastRows;
+    while (P > 0 && rows < kF8TileRows && held * ceil_div(P, held * rows) * ceil_div(N, 256) > 256) rows += 32;
+    return rows;
+}
+
+F8Layout f8_layout(int64_t T, int top_k, int E, int64_t N) {
     const int64_t P = T * top_k, C = ceil_div(P, kF8Chunk);
     F8Layout L{};
     const int64_t held = E < P ? E : P;  // experts that can have a row
     L.stream = P <= kF8InlineP || P <= kF8Mean * held ? kF8Rows : 0;
     L.max_tiles[0] = L.stream ? held : 0;
     const int64_t many = P / (L.stream + 1);  // experts that can have more rows
-    L.max_tiles[1] = P / kF8TileRows + (E < many ? E : many);
+    L.tile_rows = f8_rows_of_tiles(P, held, N);
+    L.max_tiles[1] = P / L.tile_rows + (E < many ? E : many);
+    // room for the lists whichever way is taken: more tokens never need less
+    const int64_t most[2] = {held, P / kF8LeastRows + held};
     size_t o = 0;
     L.hist = o;
     o += C > 1 ? al16((size_t)C * E * 4) : 0;
@@ -77,7 +91,7 @@ F8Layout f8_layout(int64_t T, int top_k, int E) {
     o += al16((size_t)P * 4);
     for (int i = 0; i < 2; ++i) {
         L.tiles[i] = o;
-        o += al16((size_t)L.max_tiles[i] * sizeof(Tile));
+        o += al16((size_t)most[i] * sizeof(Tile));
     }
     L.ntiles = o;
     o += 16;
@@ -117,11 +131,11 @@ __device__ void scan3_1024(int (&v)[3], int* tmp) {
 
 // How many m-tiles an expert of c rows has in a list, and how many rows each (the last
 // may have fewer): the tiles of a large expert are as even as 32 rows allow.
-__device__ __forceinline__ int f8_tiles(int c, int list, int stream) {
-    return c == 0 || (c <= stream) != (list == 0) ? 0 : list == 0 ? 1 : (c + kF8TileRows - 1) / kF8TileRows;
+__device__ __forceinline__ int f8_tiles(int c, int list, const F8Lists& l) {
+    return c == 0 || (c <= l.stream) != (list == 0) ? 0 : list == 0 ? 1 : (c + l.tile_rows - 1) / l.tile_rows;
 }
-__device__ __forceinline__ int f8_tile_rows(int c) {
-    const int n = (c + kF8TileRows - 1) / kF8TileRows;
+__device__ __forceinline__ int f8_tile_rows(int c, int most) {
+    const int n = (c + most - 1) / most;
     return ((c + 31) / 32 + n - 1) / n * 32;
 }
 
@@ -133,8 +147,8 @@ __device__ void offsets_and_tiles(const int (&cnt)[4], int (&start)[4], bool giv
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         v[0] += cnt[k];
-        v[1] += f8_tiles(cnt[k], 0, lists.stream);
-        v[2] += f8_tiles(cnt[k], 1, lists.stream);
+        v[1] += f8_tiles(cnt[k], 0, lists);
+        v[2] += f8_tiles(cnt[k], 1, lists);
     }
     const int mine[2] = {v[1], v[2]};
     scan3_1024(v, tmp);
@@ -149,7 +163,7 @@ __device__ void offsets_and_tiles(const int (&cnt)[4], int (&start)[4], bool giv
             if (!given) start[k] = v[0];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int n = f8_tiles(cnt[k], i, lists.stream);
+                const int n = f8_tiles(cnt[k], i, lists);
                 for (int q = 0; list && q < n && v[1 + i] + q < lists.max_tiles[i]; ++q)
                     lists.tiles[i][v[1 + i] + q] = Tile{e, start[k], cnt[k], q};
                 v[1 + i] += n;
@@ -248,6 +262,7 @@ struct F8Params {
     const Tile* tiles;
     const int* ntiles;
     int max_tiles;      // entries of `tiles`
+    int tile_rows;      // as in F8Lists
     const int* sorted;  // Indexed: pair of each sorted row
     // at most kF8InlineP pairs: the tile from the ids (Indexed) or offsets (Grouped)
     const int *ids, *offsets;
@@ -699,8 +714,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     Tile tile = p.tiles[id / tiles_n];  // a tile of the same group
     if (id / tiles_n >= ntiles) return;
     tile.expert = __builtin_amdgcn_readfirstlane(tile.expert);
-    const int count = __builtin_amdgcn_readfirstlane(tile.rows), step = f8_tile_rows(count), number = __builtin_amdgcn_readfirstlane(tile.number);
-    const int group = number / kF8Group * kF8Group, n = min(kF8Group, (count + kF8TileRows - 1) / kF8TileRows - group);
+    const int count = __builtin_amdgcn_readfirstlane(tile.rows), step = f8_tile_rows(count, p.tile_rows), number = __builtin_amdgcn_readfirstlane(tile.number);
+    const int group = number / kF8Group * kF8Group, n = min(kF8Group, (count + p.tile_rows - 1) / p.tile_rows - group);
     const int in_group = id - (id / tiles_n - (number - group)) * tiles_n, tn = in_group / n, m = group + in_group % n;
     tile.first += m * step;
     tile.rows = min(step, count - m * step);
@@ -719,12 +734,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }  // namespace
 
 size_t moe_f8_workspace(int64_t T, int top_k, int E) {
-    return f8_layout(T, top_k, E).bytes;
+    return f8_layout(T, top_k, E, 1).bytes;
 }
 
 hipError_t moe_f8_launch(const MoeF8Args& a) {
     const int64_t P = a.T * a.top_k;
-    const F8Layout L = f8_layout(a.T, a.top_k, a.E);
+    const F8Layout L = f8_layout(a.T, a.top_k, a.E, a.N);
     char* ws = (char*)a.ws;
     F8Params p{};
     p.A = (const uint8_t*)a.A;
@@ -753,6 +768,7 @@ hipError_t moe_f8_launch(const MoeF8Args& a) {
     int* sorted = (int*)(ws + L.sorted);
     F8Lists lists{};
     lists.stream = L.stream;
+    lists.tile_rows = p.tile_rows = L.tile_rows;
     for (int i = 0; i < 2; ++i) {
         lists.tiles[i] = (Tile*)(ws + L.tiles[i]);
         lists.max_tiles[i] = (int)L.max_tiles[i];

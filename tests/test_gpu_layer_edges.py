@@ -273,3 +273,33 @@ def test_swiglu_rows_where_the_threads_of_a_row_change(rows, I):
     gu = (1.5 * torch.randn(rows, 2 * I, generator=torch.Generator().manual_seed(I))).to(torch.bfloat16).cuda()
     for form in ("f8_token", "mx_f8"):
         check_rows(form, "bf16", ol.silu_mul(f64(gu)), SILU_DELTA, *swiglu(form, "bf16", gu, rows, I))
+
+
+@pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 1152, 8448])
+def test_experts_in_tiles_of_every_height(K):
+    """64 column tiles: from 128 to 256 rows make a tile, by the rows of the call.  The same bits as 90 rows at a time,
+    which the other tests compare with the definition."""
+    N = 16384
+    desc = hq.desc_moe_fp8_blockwise(1, N, K)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    w = torch.randint(0, 256, (N * K,), generator=g, device="cuda", dtype=torch.uint8) & 0xBF  # (no NaN)
+    s = torch.rand(K // 128 * N // 128, generator=g, device="cuda")
+    a = torch.randint(0, 256, (1300, K), generator=g, device="cuda", dtype=torch.uint8) & 0xBF
+    sa = torch.rand(1300, K // 128, generator=g, device="cuda")
+
+    def run(first, rows):
+        n = hq.hq_workspace_bytes(desc, rows, 1)
+        out = torch.full((rows * N + 64,), 3.0, dtype=torch.bfloat16, device="cuda")
+        ids = torch.zeros(rows, dtype=torch.int32, device="cuda")
+        hq.hq_moe_gemm(desc, hq.HQ_MOE_INDEXED, rows, 1, a[first:first + rows].clone(), sa[first:first + rows].clone(), ids, None, w, s, None, out,
+                       torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+        torch.cuda.synchronize()
+        assert (out[rows * N:] == 3.0).all()
+        return out[:rows * N].view(rows, N)
+
+    few = torch.cat([run(i, min(90, 1300 - i)) for i in range(0, 1300, 90)])
+    assert torch.isfinite(few.float()).all() and few.float().abs().max() > 0
+    for rows in (370, 500, 630, 760, 890, 1000, 1300):
+        note(f"experts f8 heights K={K} rows={rows}")
+        # (rows of a call come sorted in any order; D has them in the tokens')
+        assert torch.equal(run(0, rows), few[:rows])

@@ -189,3 +189,13 @@ def test_as_many_rows_as_a_launch_holds():
     for M, want in ((1 << 22, BAD), ((1 << 22) - 1, ALIGN)):
         assert status_of(hq.hq_rmsnorm, norm(), **{**NORM, "M": M, "x": A + 8}) == want
         assert status_of(hq.hq_silu_mul_quant, **{**SILU, "rows": M, "gate_up": A + 8}) == want
+
+
+@pytest.mark.parametrize("E,top_k", [(1, 1), (3, 2), (8, 8), (32, 4), (256, 8), (4096, 1)])
+def test_fewer_tokens_never_need_a_larger_workspace(E, top_k):
+    """A workspace for the largest step serves every smaller one, whichever kernels take it."""
+    desc, before = hq.desc_moe_fp8_blockwise(E, 256, 256), 0
+    for T in (*range(2200), 4095, 4096, 4097, 20000, 65535, 65536):
+        need = hq.hq_workspace_bytes(desc, T, top_k)
+        assert need >= before, T
+        before = need
