@@ -31,7 +31,7 @@ namespace {
 constexpr int kF8InlineP = 64;   // one pair per lane of a wave
 constexpr int kF8Chunk = 4096;   // pairs of one routing workgroup
 constexpr int kF8TileRows = 256; // rows of a large m-tile, at most
-constexpr int kF8LeastRows = 96; // (fewer take as long)
+constexpr int kF8LeastRows = 96; // (three subtiles of a wave: the fewest that the pipeline of loads is built for)
 constexpr int kF8Rows = 32;      // rows that the weight stream takes at a time
 // Which experts the weight stream takes: those of up to kF8Rows rows where experts have
 // up to kF8Mean rows in the mean, else none.  Two launches of which each has a part of the
