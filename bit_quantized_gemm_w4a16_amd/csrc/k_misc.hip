@@ -24,7 +24,8 @@ namespace hq {
 
 // Tokenwise E4M3 activation quantisation: one workgroup per row.
 // s = max|x| / 448 (correctly rounded fp32 division, the HIP default; 1 for
-// an all-zero row), q = E4M3(x / s)
+// an all-zero row; at least 2^-149, since the quotient of a denormal below
+// 225 units of that rounds to 0, and the row's zeros to 0 / 0), q = E4M3(x / s)
 // with round-to-nearest-even; |x / s| is clamped to 448 first, which equals
 // saturating rounding since every quotient lies within rounding of +-448.
 // Non-finite input: NaN elements take no part in the maximum (fmaxf returns
@@ -49,7 +50,7 @@ __global__ __launch_bounds__(256) void quant_e4m3_kernel(const float* __restrict
         __syncthreads();
     }
     amax = red[0];
-    const float sc = amax > 0.f ? amax / 448.0f : 1.0f;
+    const float sc = amax > 0.f ? fmaxf(amax / 448.0f, 0x1p-149f) : 1.0f;
     if (threadIdx.x == 0) s[row] = sc;
     uint8_t* qr = q + row * K;
     for (int k = 2 * threadIdx.x; k < K; k += 512) {
@@ -87,7 +88,7 @@ __global__ __launch_bounds__(256) void quant_e4m3_rows_kernel(const float4* __re
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
     __syncthreads();
     amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float sc = amax > 0.f ? amax / 448.0f : 1.0f;
+    const float sc = amax > 0.f ? fmaxf(amax / 448.0f, 0x1p-149f) : 1.0f;
     if (threadIdx.x == 0) s[row] = sc;
     uint32_t* qr = q + row * K4;
 #pragma unroll

@@ -448,7 +448,7 @@ hq_status hq_moe_gemm(const hq_layer_desc* desc, int32_t mode, int64_t T, int32_
  * Tokenwise activation quantisation ("Humming wird angekuendigt", section
  * "End-to-End-Inferenzleistung": tokenwise FP8 activations for W4A8).
  * For each row m of x (fp32 [M][K]): s[m] = max_k |x| / 448 in fp32 (1 for an
- * all-zero row); q[m][k] = E4M3(x / s[m]), fp32 division, round to nearest
+ * all-zero row; never 0: at least 2^-149); q[m][k] = E4M3(x / s[m]), fp32 division, round to nearest
  * even, saturating at +-448.  out_dtype must be HQ_DT_FP8_E4M3.
  */
 hq_status hq_quantize_act(int32_t out_dtype, int64_t M, int64_t K, const float* x, void* q, float* s,
@@ -460,7 +460,7 @@ hq_status hq_quantize_act(int32_t out_dtype, int64_t M, int64_t K, const float* 
  * "W8A8 / W4A8 / W4A4": FP8 W8A8 with blockwise scaling; block 128 gives the
  * 1 x 128 activation blocks of that path, block K the tokenwise case of
  * hq_quantize_act).  Per block: s = max |x| / 448 in fp32 (1 for an all-zero
- * block), q = E4M3(x / s) with fp32 division, round to nearest even,
+ * block; at least 2^-149), q = E4M3(x / s) with fp32 division, round to nearest even,
  * saturating at +-448; NaN and infinity as in hq_quantize_act.
  *   x fp32 [M][K], q [M][K], s fp32 [M][K/block]; K a multiple of block,
  *   block a multiple of 4 unless it equals K; pointers 16-byte aligned.

@@ -148,7 +148,8 @@ static int64_t row_of(const int64_t* rows, int64_t r) { return rows ? rows[r] : 
 /* activation quantisation (tokenwise E4M3)                             */
 /* ------------------------------------------------------------------ */
 
-/* Per row m: s[m] = max_k |x| / 448 in fp32 (1 for an all-zero row), and
+/* Per row m: s[m] = max_k |x| / 448 in fp32 (1 for an all-zero row, at least
+ * the smallest fp32 above 0 for another: no scale is 0), and
  * q[m][k] = E4M3_RNE_satfinite(x / s[m]) with the division in fp32. */
 void hq_oracle_quant_act_e4m3(int64_t M, int64_t K, const float* x, uint8_t* q, float* s)
 {
@@ -158,7 +159,7 @@ void hq_oracle_quant_act_e4m3(int64_t M, int64_t K, const float* x, uint8_t* q, 
             float a = fabsf(x[m * K + k]);
             if (a > amax) amax = a;
         }
-        float sc = (amax > 0.0f) ? amax / 448.0f : 1.0f;
+        float sc = (amax > 0.0f) ? fmaxf(amax / 448.0f, 0x1p-149f) : 1.0f;
         s[m] = sc;
         for (int64_t k = 0; k < K; ++k) {
             float v = x[m * K + k] / sc;
@@ -168,7 +169,8 @@ void hq_oracle_quant_act_e4m3(int64_t M, int64_t K, const float* x, uint8_t* q, 
 }
 
 /* Per row m and block b of B consecutive elements along K (K % B == 0):
- * s[m][b] = max |x| over the block / 448 in fp32 (1 for an all-zero block),
+ * s[m][b] = max |x| over the block / 448 in fp32 (1 for an all-zero block, at
+ * least the smallest fp32 above 0 for another),
  * q = E4M3_RNE_satfinite(x / s) with the division in fp32.  B == K is the
  * tokenwise case above; B == 128 is the 1 x 128 activation blocks of FP8
  * W8A8 with blockwise scales. */
@@ -183,7 +185,7 @@ int hq_oracle_quant_act_e4m3_blocks(int64_t M, int64_t K, int64_t B, const float
                 float a = fabsf(xb[k]);
                 if (a > amax) amax = a;
             }
-            float sc = (amax > 0.0f) ? amax / 448.0f : 1.0f;
+            float sc = (amax > 0.0f) ? fmaxf(amax / 448.0f, 0x1p-149f) : 1.0f;
             s[m * (K / B) + b] = sc;
             for (int64_t k = 0; k < B; ++k) q[m * K + b * B + k] = (uint8_t)hq_oracle_e4m3_encode(xb[k] / sc);
         }
