@@ -3,7 +3,7 @@
 //
 //   norm:    h = x + r,  y = h (mean h^2 + eps)^-1/2 (w + offset)
 //   SwiGLU:  y = silu(gate) up,  silu(g) = g / (1 + e^-g)
-//   tokens:  s = max|y| / top over the row (top: E4M3 448, INT8 127; 1 for zeros), q = rnd(y / s)
+//   tokens:  s = max|y| / top over the row (top: E4M3 448, INT8 127; 1 for zeros, never 0), q = rnd(y / s)
 //   blocks:  the same over 128 consecutive elements (E4M3)
 //   MX:      E8M0 per 32: the exponent of max|y| less emax (E4M3 8, E2M1 2), q = rnd(y 2^(127 - e))
 //
@@ -64,6 +64,10 @@ __device__ __forceinline__ uint32_t e4m3x4_below(float a, float b, float c, floa
     const uint32_t u = (uint32_t)pk;
     return u & ~(((u & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u);
 }
+
+// The scale that takes the largest value m to `top`; 1 for zeros.  Of a denormal m below some half
+// `top` units of 2^-149 the quotient is 0, and zeros would be 0 / 0: one unit at least.
+__device__ __forceinline__ float scale_of(float m, float top) { return m > 0.f ? fmaxf(m / top, 0x1p-149f) : 1.f; }
 
 // v / s for eight values, s the scale that takes the largest to `top`.  With r = 1 / s after one
 // Newton step, q0 = v r is within two units of v / s, and q0 + (v - q0 s) r within one half and
@@ -264,7 +268,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(RowParams p)
 #pragma unroll
             for (int j = 0; j < NV; ++j) m = fmaxf(m, amax8(y[j]));
             m = row_reduce<TPR, true>(m, red[1]);
-            s = m > 0.f ? m / top : 1.f;
+            s = scale_of(m, top);
             if (t == 0) ((float*)p.scale)[row] = s;
         }
 #pragma unroll
@@ -273,7 +277,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(RowParams p)
                 float m = amax8(y[j]);
 #pragma unroll
                 for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-                s = m > 0.f ? m / top : 1.f;
+                s = scale_of(m, top);
                 if ((t & 15) == 0 && el(j) < K) ((float*)p.scale)[row * (K / 128) + el(j) / 128] = s;
             }
             const int n = K - el(j);

@@ -536,8 +536,8 @@ hq_status hq_moe_gather(int32_t dtype, int64_t T, int32_t top_k, int64_t K, cons
  * in fp32 from the unrounded h, and y in one of these forms:
  *   out_dtype   a_scale        out
  *   dtype       NONE           [M][K], rounded once; out_scale NULL
- *   FP8_E4M3    PER_TOKEN_F32  as hq_quantize_act: s = max|y| / 448 per row (1 for a row of zeros)
- *   INT8        PER_TOKEN_F32  s = max|y| / 127, q = y / s to the nearest (ties to even) of -127..127; NaN gives 0
+ *   FP8_E4M3    PER_TOKEN_F32  as hq_quantize_act: s = max|y| / 448 per row (1 for a row of zeros, at least 2^-149)
+ *   INT8        PER_TOKEN_F32  s = max|y| / 127 (at least 2^-149), q = y / s to the nearest (ties to even) of -127..127; NaN gives 0
  *   FP8_E4M3    PER_BLOCK128   as hq_quantize_act_blocks with block 128 (K a multiple of 128)
  *   FP8_E4M3 | FP4_E2M1  MX_E8M0  as hq_quantize_act_mx (K a multiple of 32)
  * which are the activations of the layers with that a_dtype and a_scale.  NaN and
