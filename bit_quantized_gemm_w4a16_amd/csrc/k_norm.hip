@@ -70,7 +70,7 @@ __device__ __forceinline__ uint32_t e4m3x4_below(float a, float b, float c, floa
 __device__ __forceinline__ float scale_of(float m, float top) { return m > 0.f ? fmaxf(m / top, 0x1p-149f) : 1.f; }
 
 // v / s for eight values, s the scale that takes the largest to `top`.  With r = 1 / s after one
-// Newton step, q0 = v r is within two units of v / s, and q0 + (v - q0 s) r within one half and
+// Newton step, q0 = v r is within two units of v / s, and q0 - (q0 s - v) r within one half and
 // the little that r is off by: the rounding to 8 bits sees no difference to a division but in a
 // value within a unit of 2^-24 of a border.  Three instructions for each value in place of ten (SwiGLU,
 // 16376 rows of 2048 in blocks: 32 us, with divisions 41; the norm of 8191 rows of 7168 in
@@ -84,7 +84,7 @@ __device__ __forceinline__ void divide8(const float (&v)[8], float s, float top,
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float q0 = v[i] * r;
-            q[i] = fmaf(fmaf(-q0, s, v[i]), r, q0);
+            q[i] = fmaf(fmaf(q0, s, -v[i]), -r, q0);  // (with these signs a -0 stays one)
         }
     } else {
 #pragma unroll
