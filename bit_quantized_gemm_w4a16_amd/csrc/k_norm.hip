@@ -159,7 +159,7 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
 template <bool BF16, Quant Q, int TPR, int NV, bool VEC>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(RowParams p) {
     static_assert(VEC || Q == Quant::SAME16 || Q == Quant::TOKEN, "block scales need whole groups");
-    __shared__ float red[2][16];
+    __shared__ float red[4][16];
     constexpr int RPW = TPR < 256 ? 256 / TPR : 1;  // rows per workgroup
     const int t = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
@@ -211,7 +211,30 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(RowParams p)
             for (int i = 0; i < 8; ++i) ss += y[j][i] * y[j][i];
         }
         ss = row_reduce<TPR, false>(ss, red[0]);
-        const float rs = 1.0f / sqrtf(ss / (float)K + p.eps);
+        const float mean = ss / (float)K + p.eps;
+        float rs = 1.0f / sqrtf(mean);
+        // Squares at fp32's ends (sums of them that are denormals or 0 where eps does not cover it, or
+        // infinite): the row is brought to 1..2 by a power of two first, eps with it in 64 bits.  (A NaN,
+        // an infinity or a row of zeros has its rs already.)
+        if (!(mean > 0x1p-100f && mean < INFINITY)) {
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) m = fmaxf(m, amax8(y[j]));
+            m = row_reduce<TPR, true>(m, red[2]);
+            if (m > 0.f && m < INFINITY && ss == ss) {
+                const int e = ilogbf(m);
+                float s2 = 0.f;
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        y[j][i] = ldexpf(y[j][i], -e);
+                        s2 += y[j][i] * y[j][i];
+                    }
+                s2 = row_reduce<TPR, false>(s2, red[3]);
+                rs = (float)(1.0 / sqrt((double)s2 / K + ldexp((double)p.eps, -2 * e)));
+            }
+        }
         const uint16_t* w16 = (const uint16_t*)p.w;
         const float* w32 = (const float*)p.w;
 #pragma unroll

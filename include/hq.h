@@ -549,8 +549,10 @@ hq_status hq_moe_gather(int32_t dtype, int64_t T, int32_t top_k, int64_t K, cons
  *   out          dense [M][K] (E2M1: [M][K/2] bytes); out_scale as the table says
  * K 1..65536, M below 2^22.  Rows and strides that are multiples of 8 are the
  * fastest; others are taken too, but not with block scales (128 or MX).
- * Squares are summed in fp32: a row whose squares pass 2^127 in sum gives zeros (NaN
- * where h is infinite).  Apart from sum_out the outputs must not overlap the inputs.
+ * Squares are summed in fp32, those of a row whose mean square leaves its range at
+ * either end after a power of two; with eps 0 a row of zeros is NaN, and a row with an
+ * infinity NaN there and 0 elsewhere.  Apart from sum_out the outputs must not overlap
+ * the inputs.
  */
 typedef struct hq_norm_desc {
     int32_t abi_version;  /* HQ_ABI_VERSION                      */
