@@ -866,6 +866,8 @@ hq_status hq_rmsnorm(const hq_norm_desc* d, int64_t M, int64_t K, const void* x,
     if (!x || !weight || !out) return set_error(HQ_ERR_INVALID_ARG, "x, weight and out are required");
     if ((out_scale != nullptr) != (a.kind != RowOut::SAME16))
         return set_error(HQ_ERR_INVALID_ARG, out_scale ? "out_scale must be NULL for a 16-bit output" : "out_scale is required");
+    if (M > 1 && sum_out && ((sum_out == x && sum_stride != x_stride) || (sum_out == residual && sum_stride != residual_stride)))
+        return set_error(HQ_ERR_INVALID_ARG, "sum_out in place of x or the residual needs the same stride");
     if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(sum_out) || !aligned16(out) || !aligned16(out_scale))
         return set_error(HQ_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
     a.bf16 = d->dtype == HQ_DT_BF16;

@@ -546,6 +546,7 @@ hq_status hq_moe_gather(int32_t dtype, int64_t T, int32_t top_k, int64_t K, cons
  *                least K); residual may be NULL
  *   weight       [K], weight_dtype: dtype or FP32
  *   sum_out      dtype, or NULL; may be x or residual itself with the same stride
+ *                (another is refused)
  *   out          dense [M][K] (E2M1: [M][K/2] bytes); out_scale as the table says
  * K 1..65536, M below 2^22.  Rows and strides that are multiples of 8 are the
  * fastest; others are taken too, but not with block scales (128 or MX).
