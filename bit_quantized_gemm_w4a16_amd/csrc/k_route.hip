@@ -556,9 +556,12 @@ hipError_t go(RouteParams p, hipStream_t st) {
     const int S = p.E / p.groups, lanes = S / NE;
     p.in_lanes = S % NE == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     const size_t lds = p.groups > 1 && !p.in_lanes ? (size_t)p.E * 4 * sizeof(float) : 0;
-    static const hipError_t attr = hipFuncSetAttribute((const void*)route_kernel<NE>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                       64 * NE * 4 * (int)sizeof(float));
-    if (attr != hipSuccess) return attr;
+    // Above 64 KB in all (some 3900 experts and up, in groups that fill no whole lanes) LDS is asked for, at
+    // each call: it is granted for a kernel on one device, the current one.
+    if (lds + 4 * sizeof(Few) > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void*)route_kernel<NE>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
     hipLaunchKernelGGL((route_kernel<NE>), dim3((unsigned)((p.T + 3) / 4)), dim3(256), lds, st, p);
     return hipGetLastError();
 }
