@@ -201,7 +201,9 @@ __global__ __launch_bounds__(1024) void f8_hist_kernel(const int* __restrict__ i
     for (int e = threadIdx.x; e < E; e += 1024) hist[(int64_t)blockIdx.x * E + e] = cnt[e];
 }
 // ... and the places of its pairs, behind the experts before theirs and the chunks before its own.  One
-// chunk (hist NULL): all in one launch.  The tile lists come from the first workgroup.
+// chunk (hist NULL): all in one launch.  The tile lists come from the first workgroup.  Each workgroup reads
+// every chunk's histogram, which grows with the square of the chunks (256 experts, us: 8 chunks 9, 64 44, 256
+// 158, 1024 1150; at 256, a million pairs, the product takes some 100 times that).
 __global__ __launch_bounds__(1024) void f8_place_kernel(const int* __restrict__ ids, int64_t P, int E, const int* __restrict__ hist, int* __restrict__ sorted,
                                                         F8Lists lists) {
     __shared__ int cnt[4096];
@@ -473,6 +475,8 @@ __global__ __launch_bounds__(256) void f8_stream_kernel(F8Params p) {
 //        are in registers and its first rows (A1) read; A1(s + 2) and B(s + 2) are asked for
 // The rows' scales come four blocks at a time through registers, the weights' wait in a
 // lane each.
+// m-tiles of an expert that run side by side (32 experts of 4096 x 7168, 32760 / 16384 rows, us: one 985 / 530,
+// four 928 / 521, six 938 / 510, sixteen 957 / 516)
 constexpr int kF8Group = 6;
 constexpr int kF8Half = 128 * 128;  // bytes of A1 or A2 of a stage: 128 rows of a block
 

@@ -355,10 +355,12 @@ hipError_t go(const RowParams& p, hipStream_t st) {
 // Threads of a row by its width.  One wave as long as its registers hold the row: no barrier
 // for the sums (8191 rows, norm with a residual and scales of tokens, us: width 512 one wave
 // 9.8, four 14.3; 1024 12.5, 19.1; 2048 21.6, 26.1), but SwiGLU, which has less to wait for and
-// twice the input, from 1024 on four (2048, scales of blocks: 19.4, 17.3) unless it waits for a
-// row's scale too (tokens: 18.2, 24.8).  Then four, eight or sixteen (4096: four
+// twice the input, from 1024 on four (2048, scales of blocks: 18.3, 16.3) unless it waits for a
+// row's scale too (tokens: 17.5, 25.0).  Then four, eight or sixteen (4096: four
 // 46.6, eight 54.8; 8192 four 85.7, eight 85.1, sixteen with a group each 1.5 times as long;
-// 16384 four 178, eight 169, sixteen 171; SwiGLU 135, 138, 128).  Up to kFewRows rows the
+// 16384 four 178, eight 169, sixteen 171; SwiGLU 135, 138, 128).  Longer rows: sixteen with up to eight groups
+// a thread, of which a row just above 16384 leaves most empty (residual, tokens: 512 of 65536 44, 5.3 TB/s;
+// 2048 of 16384 43, 5.4; of 16512 62, 3.8).  Up to kFewRows rows the
 // steps of a thread count, so it has as few groups as there is a variant for (norm with scales
 // of blocks, on the card, 5 / 256 / 700 rows: 2048 one wave 5.1 / 6.0 / 6.4, four 3.2 / 3.7 /
 // 4.4; 4096 four 4.1 / 4.6 / 6.3, eight 3.4 / 4.1 / 6.2; 8192 four 5.5 / 6.6 / 9.9, eight 4.2 /
